@@ -76,6 +76,7 @@ typedef enum {
 
 typedef enum { METIS_BF16 = 0, METIS_F32 = 1 } metis_dtype;
 typedef enum { METIS_MXFP4 = 0, METIS_NVFP4 = 1 } metis_fp4_fmt;
+typedef enum { METIS_MXINT8 = 0, METIS_MXFP8 = 1 } metis_act8_fmt;
 typedef enum { METIS_SKETCH_GAUSSIAN = 0, METIS_SKETCH_SPARSE_SIGN = 1 } metis_sketch;
 
 /*
@@ -110,6 +111,46 @@ typedef struct {
   float* tensor_scale;
   float* inner_sum;
 } metis_fp4_tensor;
+
+/*
+ * One matrix kept in 8 bits, rows x cols, blocks of 32 consecutive columns
+ * under one E8M0 scale (element types of OCP MX v1.0; the last block of a row
+ * may be shorter).  It is what stays of an activation between the forward and
+ * the backward pass: 1 + 1/32 bytes an element.
+ *
+ *   codes   device, metis_act8_codes_bytes(rows, cols) bytes: rows of
+ *           32 * ceil(cols / 32) bytes; 16-byte aligned.  Bytes behind the last
+ *           column are written as 0.
+ *   scales  device, metis_act8_scales_bytes(rows, cols) bytes:
+ *           [rows][ceil(cols / 32)] scale codes.
+ *   amax    device, METIS_ACT8_AMAX floats: the largest of them is the largest
+ *           magnitude among the values held (blocks that read NaN left out);
+ *           16-byte aligned.
+ * A block with a = max|x|:
+ *   a not finite: scale code 255, codes 0; every value of the block reads NaN.
+ *   a == 0: scale code 0, codes 0.
+ *   METIS_MXINT8: se = clamp(floor(log2 a), -120, 127), code = int8 of
+ *     x * 2^(6-se) rounded to nearest even and clamped to +-127; the value is
+ *     code * 2^(se-6).
+ *   METIS_MXFP8: se = clamp(floor(log2 a) - 8, -126, 127), code = E4M3 of
+ *     x * 2^-se, nearest even, saturating at 448; the value is e4m3 * 2^se.
+ *   scale code = se + 127.
+ * (The lower clamps keep every scaling factor a normal float32.)
+ */
+#define METIS_ACT8_AMAX 1024
+
+typedef struct {
+  int32_t fmt;          /* metis_act8_fmt */
+  int64_t rows;
+  int64_t cols;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* amax;
+} metis_act8_tensor;
+
+/* Host-only helpers (no device work): buffer sizes for a metis_act8_tensor. */
+METIS_API size_t metis_act8_codes_bytes(int64_t rows, int64_t cols);
+METIS_API size_t metis_act8_scales_bytes(int64_t rows, int64_t cols);
 
 /* Host-only helpers (no device work): buffer sizes for a metis_fp4_tensor. */
 METIS_API size_t metis_fp4_codes_bytes(int64_t outer, int64_t inner);
@@ -402,6 +443,100 @@ METIS_API metis_status metis_spectral_scale(const float* G, int64_t K, int64_t N
                                   const float* U, const float* S, const float* V, int32_t k,
                                   float cap, float* Gout, void* workspace, size_t* workspace_bytes,
                                   int32_t* dev_status, void* stream);
+
+/*
+ * metis_act8_save -- an activation into 8 bits (metis_act8_tensor).
+ *   X, dtype, rows, cols, ld   device input (METIS_BF16 / METIS_F32), row-major;
+ *       any alignment of its elements, ld >= cols.
+ *   out  host struct with device buffers; out->fmt selects the format, rows and
+ *       cols must match.
+ * rows may be 0 (then only amax is written).  No workspace.
+ * The pages have no counterpart: training keeps the layer's input for the
+ * backward products, and the FP4 path quantizes it again there along the batch.
+ * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtype, fmt), METIS_ERR_SHAPE,
+ * METIS_ERR_ALIGN (X not aligned to its element, out's buffers),
+ * METIS_ERR_UNSUPPORTED, METIS_ERR_CUDA.
+ */
+METIS_API metis_status metis_act8_save(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                             metis_act8_tensor* out, void* stream);
+
+/*
+ * metis_act8_restore -- the matrix that `in` holds, as METIS_BF16 or METIS_F32
+ * (Y: rows x cols, leading dimension ld).  float32 holds every value exactly;
+ * bf16 does too, down to its subnormals (METIS_MXFP8 blocks under 2^-124 may
+ * round).  Errors as for metis_act8_save.
+ */
+METIS_API metis_status metis_act8_restore(const metis_act8_tensor* in, void* Y, int32_t dtype, int64_t ld,
+                                void* stream);
+
+/*
+ * metis_act8_quantize_fp4 -- the bytes that metis_quantize_fp4 gives for the
+ * float32 matrix that `in` holds, in one pass over the 8-bit copy: the tensor
+ * maximum of NVFP4 is taken from in->amax.
+ *   block_axis  1: blocks along the columns (out: rows x cols; the left operand
+ *       of a forward product); 0: blocks along the rows (out: cols x rows; the
+ *       left operand X^T of dW = X^T dY).  The blocked dimension must be a
+ *       multiple of 32.
+ *   out  codes, scales, tensor_scale and, optionally, scales_linear;
+ *       out->inner_sum must be NULL (METIS_ERR_UNSUPPORTED).
+ * Errors otherwise as for metis_quantize_fp4.  No workspace.
+ */
+METIS_API metis_status metis_act8_quantize_fp4(const metis_act8_tensor* in, int32_t block_axis, metis_fp4_tensor* out,
+                                     void* stream);
+
+/*
+ * metis_layer_norm_fwd -- Y = (x - mean) rstd weight + bias over the columns of
+ * every row, with mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols +
+ * eps): the norm in front of a linear layer.
+ * The pages have no counterpart: it is the layer around the split-linear layer
+ * of the models they train.
+ *   X, dtype, rows, cols, ldx   device input (METIS_BF16 / METIS_F32).
+ *   weight, bias  device, cols elements of w_dtype each, or NULL (1 and 0).
+ *   eps     >= 0.  (A constant row with eps = 0 gives NaN.)
+ *   Y, y_dtype, ldy   device output; may be X itself if ldy == ldx and
+ *           y_dtype == dtype (every row is read before it is written), and must
+ *           not overlap it otherwise.
+ *   mean, rstd  device, rows floats each, or NULL.
+ *   saved   optional (NULL: none): X in 8 bits (metis_act8_tensor, rows x cols),
+ *           the bytes metis_act8_save writes, from the same pass over X.
+ * X, Y and ld need no more alignment than their elements; rows may be 0.
+ * Statistics are float32 sums in a fixed order (the mean is corrected by the
+ * mean of the deviations, so a large common offset loses no accuracy).
+ * A row with an infinity or a NaN gives NaN in that row alone.  No workspace.
+ * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtypes, eps, fmt), METIS_ERR_SHAPE,
+ * METIS_ERR_ALIGN, METIS_ERR_UNSUPPORTED, METIS_ERR_CUDA.
+ */
+METIS_API metis_status metis_layer_norm_fwd(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                  const void* weight, const void* bias, int32_t w_dtype, float eps, void* Y,
+                                  int32_t y_dtype, int64_t ldy, float* mean, float* rstd,
+                                  metis_act8_tensor* saved, void* stream);
+
+/*
+ * metis_layer_norm_bwd -- the gradients of the norm above.  With
+ * xh = (x - mean) rstd and g = dY weight, for every row
+ *   dX = rstd (g - sum(g) / cols - xh sum(g xh) / cols)
+ * and over the rows dweight = sum(dY xh), dbias = sum(dY).
+ *   dY, g_dtype, ldg   device rows x cols.
+ *   X, x_dtype, ldx    the forward's input, or NULL and `saved` below.
+ *   saved   X in 8 bits instead of X (exactly one of the two is given); mean
+ *           and rstd are those of the exact X.
+ *   mean, rstd  device, rows floats (the forward's).
+ *   weight  device, cols elements of w_dtype, or NULL (1).
+ *   dX, dx_dtype, ldd  device rows x cols, or NULL (not wanted); may be dY
+ *           itself if ldd == ldg and dx_dtype == g_dtype, and must not overlap
+ *           an input otherwise.
+ *   dweight, dbias     device, cols floats each, or NULL (not wanted); written,
+ *           not added to.  At least one output is given.
+ * rows may be 0: dweight and dbias are then zero.  Sums over the rows are
+ * float32, in a fixed order that depends on the sizes and the device alone.
+ * Workspace: partial sums of dweight and dbias.
+ * Errors as for metis_layer_norm_fwd, and METIS_ERR_WORKSPACE.
+ */
+METIS_API metis_status metis_layer_norm_bwd(const void* dY, int32_t g_dtype, int64_t rows, int64_t cols, int64_t ldg,
+                                  const void* X, int32_t x_dtype, int64_t ldx, const metis_act8_tensor* saved,
+                                  const float* mean, const float* rstd, const void* weight, int32_t w_dtype,
+                                  void* dX, int32_t dx_dtype, int64_t ldd, float* dweight, float* dbias,
+                                  void* workspace, size_t* workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

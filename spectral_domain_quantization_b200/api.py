@@ -19,10 +19,13 @@ OK = 0
 BF16, F32 = 0, 1
 MXFP4, NVFP4 = 0, 1
 SKETCH_GAUSSIAN, SKETCH_SPARSE_SIGN = 0, 1
+MXINT8, MXFP8 = 0, 1
+ACT8_AMAX = 1024
 DEV_NUMERIC, DEV_TIMEOUT, DEV_SAMPLING = 1, 2, 4
 
 FMT = {"mx": MXFP4, "nv": NVFP4, MXFP4: MXFP4, NVFP4: NVFP4}
 FMT_NAME = {MXFP4: "mx", NVFP4: "nv"}
+ACT8_FMT = {"mxint8": MXINT8, "mxfp8": MXFP8}
 
 
 class MetisError(RuntimeError):
@@ -42,6 +45,11 @@ class FP4Struct(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("scales_linear", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
                 ("inner_sum", ctypes.c_void_p)]
+
+
+class Act8Struct(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("amax", ctypes.c_void_p)]
 
 
 class SplitParams(ctypes.Structure):
@@ -66,6 +74,7 @@ _lib = None
 _VP, _I32, _I64, _SZP = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
 _FP = ctypes.POINTER(FP4Struct)
 _OP = ctypes.POINTER(OperandStruct)
+_AP = ctypes.POINTER(Act8Struct)
 
 _SIGS = {
     "metis_fp4_codes_bytes": (ctypes.c_size_t, [_I64, _I64]),
@@ -86,6 +95,15 @@ _SIGS = {
                             _VP, _VP]),
     "metis_spectral_scale": (_I32, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _I32, ctypes.c_float, _VP, _VP, _SZP,
                                     _VP, _VP]),
+    "metis_act8_codes_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "metis_act8_scales_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "metis_act8_save": (_I32, [_VP, _I32, _I64, _I64, _I64, _AP, _VP]),
+    "metis_act8_restore": (_I32, [_AP, _VP, _I32, _I64, _VP]),
+    "metis_act8_quantize_fp4": (_I32, [_AP, _I32, _FP, _VP]),
+    "metis_layer_norm_fwd": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _I32, ctypes.c_float, _VP, _I32, _I64,
+                                    _VP, _VP, _AP, _VP]),
+    "metis_layer_norm_bwd": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _I32, _I64, _AP, _VP, _VP, _VP, _I32, _VP,
+                                    _I32, _I64, _VP, _VP, _VP, _SZP, _VP]),
 }
 
 
@@ -508,6 +526,280 @@ def spectral_scale(G, U, S, V, cap, out=None, dev_status=None):
          ctypes.c_float(cap), _ptr(out)),
         (_ptr(dev_status), _stream()), G.device, "metis_spectral_scale")
     return out
+
+
+# --------------------------------------------------------------------------
+# activations kept in 8 bits, and the layer norm
+# --------------------------------------------------------------------------
+
+_DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _matrix(t, name, device=None):
+    """Check a row-major 2-D bf16/f32 CUDA tensor (any row stride of at least
+    its width); returns its leading dimension."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a row-major 2-D tensor")
+    if t.dtype not in _DTYPE_CODE:
+        raise TypeError("only bfloat16 and float32 inputs are supported")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if cols == 0:
+        raise ValueError(f"{name} must have at least one column")
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must be a row-major 2-D tensor")
+    if rows < 2 and ld < cols:
+        ld = cols                            # the stride of at most one row is never used
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld}, {cols} columns)")
+    _on_device(t, name, device)
+    return ld
+
+
+def _on_device(t, name, device=None):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _vector(t, name, n, device, dtypes):
+    """Check a contiguous CUDA vector of n elements."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    _on_device(t, name, device)
+
+
+def _out_matrix(t, name, shape, device):
+    ld = _matrix(t, name, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return ld
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device):
+    """The current stream of `device` (a cudaStream_t as an integer)."""
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _run_on(device, fn, what, *args):
+    """fn(*args) with `device` current (the library launches on the current
+    device); args end with that device's current stream."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, _stream_of(device)), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_of(device)), what)
+
+
+class Act8:
+    """A matrix kept in 8 bits (metis_act8_tensor): rows x cols, blocks of 32
+    columns under one E8M0 scale, "mxint8" or "mxfp8" (E4M3) elements.
+
+    codes: uint8 (rows, 32 * blocks); scales: uint8 (rows, blocks) with blocks
+    = ceil(cols / 32); amax: float32 (ACT8_AMAX), whose largest is the largest
+    magnitude held.  Without buffers an empty one is allocated; a program that
+    stores an activation elsewhere (host memory, a file) keeps the three
+    tensors and passes them back in."""
+
+    def __init__(self, fmt, rows, cols, device="cuda", codes=None, scales=None, amax=None):
+        if fmt not in ACT8_FMT:
+            raise ValueError("the 8-bit formats are mxint8 and mxfp8")
+        self.fmt, self.rows, self.cols = fmt, int(rows), int(cols)
+        if self.rows < 0 or self.cols < 1:
+            raise ValueError("an 8-bit matrix has at least 0 rows and 1 column")
+        self.blocks = nb = (self.cols + 31) // 32
+        if codes is None and scales is None and amax is None:
+            codes = torch.empty((self.rows, 32 * nb), dtype=torch.uint8, device=device)
+            scales = torch.empty((self.rows, nb), dtype=torch.uint8, device=device)
+            amax = torch.empty(ACT8_AMAX, dtype=torch.float32, device=device)
+        else:
+            for name, t, shape, dt in (("codes", codes, (self.rows, 32 * nb), torch.uint8),
+                                       ("scales", scales, (self.rows, nb), torch.uint8),
+                                       ("amax", amax, (ACT8_AMAX,), torch.float32)):
+                if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != dt \
+                        or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
+                _on_device(t, name, codes.device)
+        self.codes, self.scales, self.amax = codes, scales, amax
+        self.device = codes.device
+        self._s = Act8Struct(ACT8_FMT[fmt], self.rows, self.cols, codes.data_ptr(), scales.data_ptr(),
+                             amax.data_ptr())
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel() + 4 * ACT8_AMAX
+
+
+def _act8_out(out, fmt, rows, cols, device):
+    if out is None:
+        return Act8(fmt, rows, cols, device)
+    if not isinstance(out, Act8) or (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
+        raise ValueError(f"out must be an Act8 of {rows} x {cols} in {fmt}")
+    _on_device(out.codes, "out", device)
+    return out
+
+
+def save_act8(X, fmt="mxint8", out=None):
+    """Put an activation (2-D bf16/f32 CUDA tensor, any row stride) into 8 bits
+    (metis_act8_save); returns an Act8."""
+    ld = _matrix(X, "X")
+    rows, cols = X.shape
+    out = _act8_out(out, fmt, rows, cols, X.device)
+    _run_on(X.device, lib().metis_act8_save, "metis_act8_save",
+            X.data_ptr(), _DTYPE_CODE[X.dtype], rows, cols, ld, ctypes.byref(out._s))
+    return out
+
+
+def restore_act8(a, dtype=torch.bfloat16, out=None):
+    """The matrix an Act8 holds, in bf16 or f32 (metis_act8_restore)."""
+    if not isinstance(a, Act8):
+        raise TypeError("a must be an Act8")
+    if out is None:
+        if dtype not in _DTYPE_CODE:
+            raise TypeError("only bfloat16 and float32 outputs are supported")
+        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.device)
+        ld = a.cols
+    else:
+        ld = _out_matrix(out, "out", (a.rows, a.cols), a.device)
+    _run_on(a.device, lib().metis_act8_restore, "metis_act8_restore",
+            ctypes.byref(a._s), out.data_ptr(), _DTYPE_CODE[out.dtype], ld)
+    return out
+
+
+def quantize_fp4_act8(a, fmt, axis=1, linear=False, out=None):
+    """quantize_fp4 of the float32 matrix an Act8 holds, in one pass over the 8
+    bits (metis_act8_quantize_fp4): axis 0 gives the X^T operand of
+    dW = X^T dY."""
+    if not isinstance(a, Act8):
+        raise TypeError("a must be an Act8")
+    if axis not in (0, 1):
+        raise ValueError("axis is 0 or 1")
+    outer, inner = (a.rows, a.cols) if axis == 1 else (a.cols, a.rows)
+    if inner % 32 or outer == 0 or inner == 0:
+        raise ValueError(f"the blocked dimension must be a multiple of 32 (it is {inner}) and no dimension 0")
+    if out is None:
+        out = QTensor(fmt, outer, inner, a.device, linear=linear)
+    elif (out.fmt, out.outer, out.inner) != (FMT[fmt], outer, inner) or out.codes.device != a.device:
+        raise ValueError(f"out must be a QTensor of {outer} x {inner} on {a.device}")
+    _run_on(a.device, lib().metis_act8_quantize_fp4, "metis_act8_quantize_fp4",
+            ctypes.byref(a._s), axis, ctypes.byref(out.struct()))
+    return out
+
+
+class LayerNorm:
+    """Outputs of layer_norm_fwd: Y, mean and rstd (None without stats) and
+    saved, the input in 8 bits (None unless asked for)."""
+
+    __slots__ = ("Y", "mean", "rstd", "saved")
+
+    def __init__(self, Y, mean, rstd, saved):
+        self.Y, self.mean, self.rstd, self.saved = Y, mean, rstd, saved
+
+
+def _affine(weight, bias, cols, device):
+    """Pointers of weight and bias (either may be None) and their dtype code."""
+    dt = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _vector(t, name, cols, device, _DTYPE_CODE)
+            if dt is not None and t.dtype != dt:
+                raise TypeError("weight and bias must have one dtype")
+            dt = t.dtype
+    return (None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+            BF16 if dt is None else _DTYPE_CODE[dt])
+
+
+def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=None, stats=True, out=None):
+    """Layer norm over the columns of X (metis_layer_norm_fwd).
+
+    X: 2-D bf16/f32 CUDA tensor, any row stride; weight, bias: vectors (bf16 or
+    f32) or None.  out_dtype: dtype of Y (X's).  save: "mxint8" or "mxfp8" also
+    keeps X in 8 bits, from the same pass; pass the result's ``saved`` to
+    layer_norm_bwd in place of X.  stats=False: Y alone (inference).  out: Y's
+    tensor (X itself is allowed if it has Y's dtype)."""
+    ldx = _matrix(X, "X")
+    dev = X.device
+    rows, cols = X.shape
+    w, b, wdt = _affine(weight, bias, cols, dev)
+    if not eps >= 0:
+        raise ValueError("eps must be 0 or more")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype or X.dtype, device=dev)
+        if out.dtype not in _DTYPE_CODE:
+            raise TypeError("only bfloat16 and float32 outputs are supported")
+        ldy = cols
+    else:
+        ldy = _out_matrix(out, "out", (rows, cols), dev)
+    saved = None if save is None else Act8(save, rows, cols, dev)
+    mean = rstd = mp = rp = None
+    if stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    _run_on(dev, lib().metis_layer_norm_fwd, "metis_layer_norm_fwd",
+            X.data_ptr(), _DTYPE_CODE[X.dtype], rows, cols, ldx, w, b, wdt, eps, out.data_ptr(),
+            _DTYPE_CODE[out.dtype], ldy, mp, rp, None if saved is None else ctypes.byref(saved._s))
+    return LayerNorm(out, mean, rstd, saved)
+
+
+def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True, want_dw=True, want_db=True,
+                   out=None):
+    """(dX, dweight, dbias) of layer_norm_fwd (metis_layer_norm_bwd).
+
+    X: the forward's input, or the Act8 it kept; mean, rstd: the forward's.
+    out_dtype: dtype of dX (dY's); dweight and dbias are float32.  An output
+    that is not wanted is None."""
+    ldg = _matrix(dY, "dY")
+    dev = dY.device
+    rows, cols = dY.shape
+    if not (want_dx or want_dw or want_db):
+        raise ValueError("at least one gradient must be wanted")
+    xp, xdt, ldx, sp = None, BF16, cols, None
+    if isinstance(X, Act8):
+        if (X.rows, X.cols) != (rows, cols):
+            raise ValueError(f"X is {X.rows} x {X.cols}, dY {rows} x {cols}")
+        _on_device(X.codes, "X", dev)
+        sp = ctypes.byref(X._s)
+    else:
+        ldx = _matrix(X, "X", dev)
+        if X.shape != dY.shape:
+            raise ValueError(f"X is {tuple(X.shape)}, dY {tuple(dY.shape)}")
+        xp, xdt = X.data_ptr(), _DTYPE_CODE[X.dtype]
+    _vector(mean, "mean", rows, dev, (torch.float32,))
+    _vector(rstd, "rstd", rows, dev, (torch.float32,))
+    w, _, wdt = _affine(weight, None, cols, dev)
+    ldd, dp, ddt = cols, None, BF16
+    if want_dx:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=out_dtype or dY.dtype, device=dev)
+            if out.dtype not in _DTYPE_CODE:
+                raise TypeError("only bfloat16 and float32 outputs are supported")
+        else:
+            ldd = _out_matrix(out, "out", (rows, cols), dev)
+        dp, ddt = out.data_ptr(), _DTYPE_CODE[out.dtype]
+    else:
+        out = None
+    dw = torch.empty(cols, dtype=torch.float32, device=dev) if want_dw else None
+    db = torch.empty(cols, dtype=torch.float32, device=dev) if want_db else None
+    size = ctypes.c_size_t(0)
+    args = (dY.data_ptr(), _DTYPE_CODE[dY.dtype], rows, cols, ldg, xp, xdt, ldx, sp,
+            mean.data_ptr() if rows else None, rstd.data_ptr() if rows else None, w, wdt, dp, ddt, ldd,
+            None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
+    fn = lib().metis_layer_norm_bwd
+    _run_on(dev, fn, "metis_layer_norm_bwd (workspace query)", *args, None, ctypes.byref(size))
+    # a workspace of this call alone: it stays with the stream's allocator, or
+    # with the graph that captures the call
+    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    _run_on(dev, fn, "metis_layer_norm_bwd", *args, ws.data_ptr(), ctypes.byref(size))
+    return out, dw, db
 
 
 def selftest_wait_timeout(limit_ns=1_000_000, device="cuda"):

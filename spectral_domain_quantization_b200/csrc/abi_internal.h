@@ -19,4 +19,10 @@ metis_status enqueue_quantize(const void* X, int dtype, int64_t rows, int64_t co
                               const unsigned* amax_bits_in, float* r_tap, Carver& ws,
                               cudaStream_t s);
 
+// Sizes of a matrix whose rows may be none; row-major with ld >= cols, any
+// alignment of its elements (X may be NULL when rows == 0).
+metis_status check_extent(int64_t rows, int64_t cols);
+metis_status check_any_dense(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld);
+metis_status check_act8(const metis_act8_tensor* t);
+
 }  // namespace metis

@@ -1,0 +1,537 @@
+// Activations kept in 8 bits between the forward and the backward pass: the
+// 8-bit copy of a matrix, its way back to bf16 / f32, and the FP4 operand of
+// dW = X^T dY made from it in one pass.
+//
+// All three kernels are bound by HBM: a copy moves 2 (bf16) or 4 bytes in and
+// 1 + 1/32 out per element, or the reverse; the FP4 pass reads 1 + 1/32 and
+// writes 1/2 + 1/16 (NVFP4) or 1/2 + 1/32.
+#include "act8.cuh"
+#include "act8.h"
+#include "fp4_block.cuh"
+
+namespace metis {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// unit -> (row, unit in the row), by a 32-bit division where the count allows
+struct UnitMap {
+  int64_t total;
+  int64_t per_row;
+  bool narrow;
+  MDEV void split(int64_t u, int64_t& row, int64_t& k) const {
+    if (narrow) {
+      const uint32_t r = static_cast<uint32_t>(u) / static_cast<uint32_t>(per_row);
+      row = r;
+      k = static_cast<uint32_t>(u) - r * static_cast<uint32_t>(per_row);
+    } else {
+      row = u / per_row;
+      k = u - row * per_row;
+    }
+  }
+};
+
+UnitMap unit_map(int64_t rows, int64_t per_row) {
+  UnitMap m;
+  m.per_row = per_row;
+  m.total = rows * per_row;
+  m.narrow = m.total < (int64_t{1} << 31);
+  return m;
+}
+
+MDEV float load1(const float* p) { return *p; }
+MDEV float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+MDEV void store1(float* p, float v) { *p = v; }
+MDEV void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+MDEV float cta_max(float m) {
+  __shared__ float wm[kThreads / 32];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wm[i]);
+  return m;
+}
+
+// 8 elements a thread, a block in 4 adjacent lanes (16-byte aligned rows):
+// loads of 16 bytes, code stores of 8, both contiguous over the warp.
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t cols, int64_t ld, Act8View out,
+                                                             UnitMap map) {
+  constexpr int kU = 4;                          // units in flight per thread
+  constexpr int kWords = sizeof(T) == 2 ? 1 : 2;  // 16-byte words of a unit
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  float top = 0.f;
+  // a multiple of 32 units per step: the loop's bound is the same for a warp
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - (threadIdx.x & 31) < map.total;
+       u0 += kU * stride) {
+    uint4 raw[kU][kWords];
+    int64_t row[kU], k[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t u = u0 + i * stride;
+      row[i] = k[i] = 0;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) raw[i][w] = make_uint4(0, 0, 0, 0);
+      if (u < map.total) {
+        map.split(u, row[i], k[i]);
+        const T* src = X + row[i] * ld + 8 * k[i];
+        const int64_t left = cols - 8 * k[i];
+        if (left >= 8) {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) raw[i][w] = __ldcs(reinterpret_cast<const uint4*>(src) + w);
+        } else {
+          T* e = reinterpret_cast<T*>(raw[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) e[j] = src[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t u = u0 + i * stride;
+      float v[8];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const uint32_t x[4] = {raw[i][w].x, raw[i][w].y, raw[i][w].z, raw[i][w].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (sizeof(T) == 2) {
+            v[2 * j] = __uint_as_float(x[j] << 16);
+            v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+          } else {
+            v[4 * w + j] = __uint_as_float(x[j]);
+          }
+        }
+      }
+      float a = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a = max_nan(a, fabsf(v[j]));
+      a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+      a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+      if (u < map.total) {
+        float enc;
+        const uint32_t sc = act8_scale<FMT>(a, enc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= enc;
+        uint2 codes = act8_pack8<FMT>(v);
+        if (sc == 255u) codes = make_uint2(0u, 0u);
+        __stcs(reinterpret_cast<uint2*>(out.codes + row[i] * out.ldc + 8 * k[i]), codes);
+        if ((k[i] & 3) == 0) out.scales[row[i] * out.blocks + (k[i] >> 2)] = static_cast<uint8_t>(sc);
+        top = fmaxf(top, act8_block_amax<FMT>(a, enc, sc));
+      }
+    }
+  }
+  act8_write_amax(out.amax, cta_max(top));
+}
+
+// One column a lane, a block a warp: rows that start anywhere.
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kThreads) act8_save_any_kernel(const T* X, int64_t cols, int64_t ld, Act8View out,
+                                                                 UnitMap map) {
+  constexpr int kU = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  float top = 0.f;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u0 < map.total;
+       u0 += kU * stride) {
+    float v[kU];
+    int64_t row[kU], k[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t u = u0 + i * stride;
+      v[i] = 0.f;
+      row[i] = k[i] = 0;
+      if (u < map.total) {
+        map.split(u, row[i], k[i]);
+        const int64_t c = 32 * k[i] + lane;
+        if (c < cols) v[i] = load1(X + row[i] * ld + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (u0 + i * stride >= map.total) break;   // the same for the whole warp
+      // the bits of |x| order like the values, with NaN above infinity
+      const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[i]) & 0x7FFFFFFFu));
+      float enc;
+      const uint32_t sc = act8_scale<FMT>(a, enc);
+      uint32_t code = act8_code<FMT>(v[i] * enc);
+      if (sc == 255u) code = 0u;
+      out.codes[row[i] * out.ldc + 32 * k[i] + lane] = static_cast<uint8_t>(code);
+      if (lane == 0) out.scales[row[i] * out.blocks + k[i]] = static_cast<uint8_t>(sc);
+      top = fmaxf(top, act8_block_amax<FMT>(a, enc, sc));
+    }
+  }
+  act8_write_amax(out.amax, cta_max(top));
+}
+
+// 16 elements a thread (16-byte loads of codes), 16-byte aligned output rows.
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View in, int64_t cols, T* Y, int64_t ld,
+                                                                UnitMap map) {
+  constexpr int kU = 4;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 < map.total; u0 += kU * stride) {
+    uint4 raw[kU];
+    uint32_t sc[kU];
+    int64_t row[kU], k[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t u = u0 + i * stride;
+      row[i] = k[i] = 0;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      sc[i] = 0;
+      if (u < map.total) {
+        map.split(u, row[i], k[i]);
+        raw[i] = __ldcs(reinterpret_cast<const uint4*>(in.codes + row[i] * in.ldc) + k[i]);
+        sc[i] = in.scales[row[i] * in.blocks + (k[i] >> 1)];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (u0 + i * stride >= map.total) continue;
+      const float f = act8_factor<FMT>(sc[i]);
+      float v[16];
+      act8_elems4<FMT>(raw[i].x, v);
+      act8_elems4<FMT>(raw[i].y, v + 4);
+      act8_elems4<FMT>(raw[i].z, v + 8);
+      act8_elems4<FMT>(raw[i].w, v + 12);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] *= f;
+      T* dst = Y + row[i] * ld + 16 * k[i];
+      const int64_t left = cols - 16 * k[i];
+      if (left >= 16) {
+        if constexpr (sizeof(T) == 2) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+          __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            __stcs(reinterpret_cast<float4*>(dst) + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < left) store1(dst + j, v[j]);
+      }
+    }
+  }
+}
+
+// One column a lane, a block a warp: output rows that start anywhere.
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kThreads) act8_restore_any_kernel(Act8View in, int64_t cols, T* Y, int64_t ld,
+                                                                    UnitMap map) {
+  constexpr int kU = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u0 < map.total;
+       u0 += kU * stride) {
+    uint32_t code[kU], sc[kU];
+    int64_t row[kU], k[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t u = u0 + i * stride;
+      code[i] = sc[i] = 0;
+      row[i] = k[i] = 0;
+      if (u < map.total) {
+        map.split(u, row[i], k[i]);
+        code[i] = in.codes[row[i] * in.ldc + 32 * k[i] + lane];
+        sc[i] = in.scales[row[i] * in.blocks + k[i]];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t c = 32 * k[i] + lane;
+      if (u0 + i * stride < map.total && c < cols)
+        store1(Y + row[i] * ld + c, act8_elem<FMT>(code[i]) * act8_factor<FMT>(sc[i]));
+    }
+  }
+}
+
+int grid_for(const void* kernel, int64_t ctas, int num_sms) {
+  // no more CTAs than are resident at once: the loops are grid-strided
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) != cudaSuccess || per_sm < 1)
+    per_sm = 1;
+  const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX);
+  return static_cast<int>(imax64(1, imin64(ctas, most)));
+}
+
+template <int FMT, typename T>
+void save_t(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
+  if ((reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0) {
+    const UnitMap map = unit_map(rows, 4 * out.blocks);
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_save_kernel<FMT, T>),
+                              (map.total + kThreads - 1) / kThreads, num_sms);
+    act8_save_kernel<FMT, T><<<grid, kThreads, 0, s>>>(X, cols, ld, out, map);
+  } else {
+    const UnitMap map = unit_map(rows, out.blocks);
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_save_any_kernel<FMT, T>),
+                              (map.total + kThreads / 32 - 1) / (kThreads / 32), num_sms);
+    act8_save_any_kernel<FMT, T><<<grid, kThreads, 0, s>>>(X, cols, ld, out, map);
+  }
+}
+
+template <int FMT, typename T>
+void restore_t(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
+  if ((reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0) {
+    const UnitMap map = unit_map(rows, (cols + 15) / 16);
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_restore_kernel<FMT, T>),
+                              (map.total + kThreads - 1) / kThreads, num_sms);
+    act8_restore_kernel<FMT, T><<<grid, kThreads, 0, s>>>(in, cols, Y, ld, map);
+  } else {
+    const UnitMap map = unit_map(rows, in.blocks);
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_restore_any_kernel<FMT, T>),
+                              (map.total + kThreads / 32 - 1) / (kThreads / 32), num_sms);
+    act8_restore_any_kernel<FMT, T><<<grid, kThreads, 0, s>>>(in, cols, Y, ld, map);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8 bits -> FP4
+// ---------------------------------------------------------------------------
+
+struct Act8QuantParams {
+  Act8View in;
+  int64_t rows, cols;
+  int64_t outer, inner;
+  int64_t scale_cols;        // padded scale columns of the tensor-core layout
+  uint8_t* codes;
+  uint8_t* scales;
+  uint8_t* scales_linear;    // optional
+  float* tensor_scale;
+  int64_t otiles, itiles;    // tiles over the padded outer and inner indices
+};
+
+// A CTA takes tiles of 128 outer indices x 8 blocks (axis 0) or 128 inner
+// indices (axis 1).  The scales of such a tile are whole 512-byte chunks of the
+// tensor-core layout: they are gathered in shared memory, padding included, and
+// written as contiguous 16-byte words, so the call needs no clearing pass over
+// them.  NVFP4's tensor maximum comes with the 8-bit copy, so there is no pass
+// for it either.
+//  * axis 1 (blocks along the columns): a thread takes 32 columns of a row.
+//  * axis 0 (blocks along the rows): a warp takes one block of rows of 128
+//    columns and reads 4 columns a lane, 128 bytes a row.  A row's 4 block
+//    scales (the 8-bit blocks run along the columns) come as one byte a lane
+//    for 8 rows, by shuffle.  The codes of a column are put together in shared
+//    memory and leave as contiguous 64 (NVFP4) or 128 bytes a column.
+template <int FMT8, int FMT4, int AXIS>
+__global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantParams p) {
+  constexpr int kBlk = FMT4 == METIS_NVFP4 ? 16 : 32;
+  constexpr int kTi = AXIS == 0 ? 8 * kBlk : 128;  // inner indices of a tile
+  constexpr int kNb = kTi / kBlk;                  // FP4 blocks along a tile
+  constexpr int kLdc = kTi / 2 + 8;                // bytes between columns of code_tile: 8-byte stores of 16 lanes
+                                                   // then fall on different banks
+  __shared__ float enc_tab[128];
+  __shared__ __align__(16) uint8_t sc_tile[128 * kNb];
+  __shared__ __align__(16) uint8_t code_tile[AXIS == 0 ? 128 * kLdc : 16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float s_t = 1.f;
+  if (FMT4 == METIS_NVFP4) {
+    float m = 0.f;
+    for (int i = tid; i < METIS_ACT8_AMAX; i += kThreads) m = fmaxf(m, p.in.amax[i]);
+    s_t = nv_tensor_scale(cta_max(m));
+    nv_enc_table(s_t, enc_tab);
+    if (blockIdx.x == 0 && tid == 0) *p.tensor_scale = s_t;
+    __syncthreads();
+  }
+  const int64_t tiles = p.otiles * p.itiles;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t ot = t / p.itiles;
+    const int64_t o0 = ot * 128, i0 = (t - ot * p.itiles) * kTi;
+    if (AXIS == 1) {
+      // 512 units of 32 columns: a row's 4 units in adjacent lanes
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = tid + kThreads * h, r = e >> 2, u = e & 3;
+        const int64_t o = o0 + r, c = i0 + 32 * u;
+        uint32_t sc4[2] = {0, 0};
+        if (o < p.outer && c < p.inner) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.in.codes + o * p.in.ldc + c);
+          const uint4 a = src[0], b = src[1];
+          const float f = act8_factor<FMT8>(p.in.scales[o * p.in.blocks + (c >> 5)]);
+          float v[32];
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) act8_elems4<FMT8>(w[j], v + 4 * j);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
+          uint64_t pk[2];
+          if (FMT4 == METIS_NVFP4) {
+            sc4[0] = quant_block_nv_tab(v, s_t, enc_tab, pk[0]);
+            sc4[1] = quant_block_nv_tab(v + 16, s_t, enc_tab, pk[1]);
+          } else {
+            float unused;
+            sc4[0] = quant_block_mx(v, pk, unused);
+          }
+          *reinterpret_cast<uint4*>(p.codes + o * (p.inner / 2) + c / 2) =
+              make_uint4(static_cast<uint32_t>(pk[0]), static_cast<uint32_t>(pk[0] >> 32),
+                         static_cast<uint32_t>(pk[1]), static_cast<uint32_t>(pk[1] >> 32));
+          if (p.scales_linear) {
+#pragma unroll
+            for (int b2 = 0; b2 < 32 / kBlk; ++b2)
+              p.scales_linear[o * (p.inner / kBlk) + c / kBlk + b2] = static_cast<uint8_t>(sc4[b2]);
+          }
+        }
+#pragma unroll
+        for (int b2 = 0; b2 < 32 / kBlk; ++b2)
+          sc_tile[tc_scale_offset(r, u * (32 / kBlk) + b2, kNb)] = static_cast<uint8_t>(sc4[b2]);
+      }
+    } else {
+      // outer = columns of X, inner = its rows; warps over the blocks of rows
+      const int64_t c = o0 + 4 * lane;                   // this lane's 4 columns
+      {
+        const int b = warp;                              // 8 warps, 8 blocks
+        const int64_t r0 = i0 + b * kBlk;
+        uint32_t sc4 = 0;                                // the 4 columns' scale codes
+        uint32_t pk[4][kBlk / 8] = {};
+        if (r0 < p.inner) {                              // whole blocks: inner is a multiple of 32
+          uint32_t raw[kBlk];
+          uint32_t sb[kBlk / 8];
+          const bool in = c < p.in.ldc;
+          const uint8_t* src = p.in.codes + r0 * p.in.ldc + c;
+#pragma unroll
+          for (int j = 0; j < kBlk; ++j) raw[j] = in ? *reinterpret_cast<const uint32_t*>(src + j * p.in.ldc) : 0u;
+          const int64_t blk = (o0 >> 5) + (lane & 3);
+#pragma unroll
+          for (int j = 0; j < kBlk / 8; ++j)
+            sb[j] = blk < p.in.blocks ? p.in.scales[(r0 + 8 * j + (lane >> 2)) * p.in.blocks + blk] : 0u;
+          float f[kBlk];
+#pragma unroll
+          for (int j = 0; j < kBlk; ++j)
+            f[j] = act8_factor<FMT8>(__shfl_sync(0xFFFFFFFFu, sb[j >> 3], 4 * (j & 7) + (lane >> 3)));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v[kBlk];
+#pragma unroll
+            for (int j = 0; j < kBlk; ++j) v[j] = __fmul_rn(act8_elem_at<FMT8>(raw[j], q), f[j]);
+            uint32_t code;
+            if (FMT4 == METIS_NVFP4) {
+              uint64_t w;
+              code = quant_block_nv_tab(v, s_t, enc_tab, w);
+              pk[q][0] = static_cast<uint32_t>(w);
+              pk[q][1] = static_cast<uint32_t>(w >> 32);
+            } else {
+              uint64_t w[2];
+              float unused;
+              code = quant_block_mx(v, w, unused);
+              pk[q][0] = static_cast<uint32_t>(w[0]);
+              pk[q][1] = static_cast<uint32_t>(w[0] >> 32);
+              pk[q][2 % (kBlk / 8)] = static_cast<uint32_t>(w[1]);
+              pk[q][3 % (kBlk / 8)] = static_cast<uint32_t>(w[1] >> 32);
+            }
+            if (c + q >= p.outer) code = 0u;             // padding columns: scale 0
+            sc4 |= code << (8 * q);
+            if (p.scales_linear && c + q < p.outer)
+              p.scales_linear[(c + q) * (p.inner / kBlk) + r0 / kBlk] = static_cast<uint8_t>(code);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sc_tile[tc_scale_offset(4 * lane + q, b, kNb)] = static_cast<uint8_t>(sc4 >> (8 * q));
+          uint8_t* dst = code_tile + (32 * q + lane) * kLdc + b * (kBlk / 2);   // column 4 lane + q
+#pragma unroll
+          for (int w = 0; w < kBlk / 8; w += 2) *reinterpret_cast<uint2*>(dst + 4 * w) = make_uint2(pk[q][w], pk[q][w + 1]);
+        }
+      }
+    }
+    __syncthreads();
+    if (AXIS == 0) {
+      constexpr int kW = kTi / 32;                       // 16-byte words a column (32 rows each)
+#pragma unroll
+      for (int h = 0; h < 128 * kW / kThreads; ++h) {
+        const int e = tid + kThreads * h, cc = e / kW, w = e % kW;
+        const int64_t o = o0 + cc, r = i0 + 32 * w;
+        if (o < p.outer && r < p.inner) {
+          const uint2* q = reinterpret_cast<const uint2*>(code_tile + (32 * (cc & 3) + (cc >> 2)) * kLdc + 16 * w);
+          *reinterpret_cast<uint4*>(p.codes + o * (p.inner / 2) + r / 2) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+        }
+      }
+    }
+    if (tid < 8 * kNb)   // 128 kNb bytes of scales: contiguous chunks of the layout
+      *reinterpret_cast<uint4*>(p.scales + tc_scale_offset(o0, i0 / kBlk, p.scale_cols) + 16 * tid) =
+          *reinterpret_cast<const uint4*>(sc_tile + 16 * tid);
+    __syncthreads();
+  }
+}
+
+template <int FMT8, int FMT4>
+void quantize_t(const Act8QuantParams& p, int axis, int num_sms, cudaStream_t s) {
+  const int64_t tiles = p.otiles * p.itiles;
+  if (axis == 1) {
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 1>), tiles, num_sms);
+    act8_quantize_kernel<FMT8, FMT4, 1><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    const int grid = grid_for(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 0>), tiles, num_sms);
+    act8_quantize_kernel<FMT8, FMT4, 0><<<grid, kThreads, 0, s>>>(p);
+  }
+}
+
+}  // namespace
+
+void launch_act8_save(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, const Act8View& out,
+                      int num_sms, cudaStream_t s) {
+  const bool i8 = out.fmt == METIS_MXINT8;
+  if (dtype == METIS_BF16) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(X);
+    i8 ? save_t<METIS_MXINT8>(x, rows, cols, ld, out, num_sms, s)
+       : save_t<METIS_MXFP8>(x, rows, cols, ld, out, num_sms, s);
+  } else {
+    const float* x = static_cast<const float*>(X);
+    i8 ? save_t<METIS_MXINT8>(x, rows, cols, ld, out, num_sms, s)
+       : save_t<METIS_MXFP8>(x, rows, cols, ld, out, num_sms, s);
+  }
+}
+
+void launch_act8_restore(const Act8View& in, int64_t rows, int64_t cols, void* Y, int dtype, int64_t ld, int num_sms,
+                         cudaStream_t s) {
+  const bool i8 = in.fmt == METIS_MXINT8;
+  if (dtype == METIS_BF16) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(Y);
+    i8 ? restore_t<METIS_MXINT8>(in, rows, cols, y, ld, num_sms, s)
+       : restore_t<METIS_MXFP8>(in, rows, cols, y, ld, num_sms, s);
+  } else {
+    float* y = static_cast<float*>(Y);
+    i8 ? restore_t<METIS_MXINT8>(in, rows, cols, y, ld, num_sms, s)
+       : restore_t<METIS_MXFP8>(in, rows, cols, y, ld, num_sms, s);
+  }
+}
+
+void launch_act8_quantize(const Act8View& in, int64_t rows, int64_t cols, int axis, const metis_fp4_tensor* out,
+                          int num_sms, cudaStream_t s) {
+  Act8QuantParams p{};
+  p.in = in;
+  p.rows = rows;
+  p.cols = cols;
+  p.outer = out->outer;
+  p.inner = out->inner;
+  p.scale_cols = tc_scale_cols(out->fmt, out->inner);
+  p.codes = out->codes;
+  p.scales = out->scales;
+  p.scales_linear = out->scales_linear;
+  p.tensor_scale = out->tensor_scale;
+  p.otiles = tc_scale_rows(p.outer) / 128;
+  const int blk = out->fmt == METIS_NVFP4 ? 16 : 32;
+  p.itiles = p.scale_cols * blk / (axis == 0 ? 8 * blk : 128);   // the padded scale columns too
+  const bool i8 = in.fmt == METIS_MXINT8, nv = out->fmt == METIS_NVFP4;
+  if (i8)
+    nv ? quantize_t<METIS_MXINT8, METIS_NVFP4>(p, axis, num_sms, s)
+       : quantize_t<METIS_MXINT8, METIS_MXFP4>(p, axis, num_sms, s);
+  else
+    nv ? quantize_t<METIS_MXFP8, METIS_NVFP4>(p, axis, num_sms, s)
+       : quantize_t<METIS_MXFP8, METIS_MXFP4>(p, axis, num_sms, s);
+}
+
+}  // namespace metis

@@ -1,0 +1,141 @@
+// One block of an activation kept in 8 bits: 32 consecutive columns under one
+// E8M0 scale (OCP MX v1.0 element types).
+//
+//   a = max |x| of the block.
+//   a not finite: scale code 255, codes 0 (every value of the block reads NaN)
+//   a == 0:       scale code 0, codes 0
+//   MXINT8: se = clamp(floor(log2 a), -120, 127);
+//           code = rne(x 2^(6 - se)) clamped to +-127, value = code 2^(se - 6)
+//   MXFP8:  se = clamp(floor(log2 a) - 8, -126, 127);
+//           code = E4M3 rne(x 2^-se) saturating at 448, value = e4m3 2^se
+//   scale code = se + 127.
+// Every scaling is by a normal power of two, so the one rounding is the
+// element's.  (A lower clamp than the E8M0 range's, so that no factor is
+// subnormal: blocks whose maximum is under 2^-120 keep an absolute step.)
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace metis {
+
+// max that returns NaN if either operand is NaN
+MDEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Scale code of a block with maximum a >= 0 (or NaN), and 2^(6 - se) or 2^-se.
+template <int FMT>
+MDEV uint32_t act8_scale(float a, float& enc) {
+  const int e = static_cast<int>(__float_as_uint(a) >> 23) - 127;  // floor(log2 a), -127 for subnormals and 0
+  const int se = FMT == METIS_MXINT8 ? max(e, -120) : max(e - 8, -126);
+  enc = __uint_as_float(static_cast<uint32_t>(FMT == METIS_MXINT8 ? 133 - se : 127 - se) << 23);
+  if (e == 128) return 255u;  // infinity or NaN
+  return a == 0.f ? 0u : static_cast<uint32_t>(se + 127);
+}
+
+// 8 scaled values (x enc) -> 8 code bytes, element i in byte i.
+template <int FMT>
+MDEV uint2 act8_pack8(const float* q) {
+  uint2 r;
+  if (FMT == METIS_MXINT8) {
+    // 1.5 2^23 + q rounds q to the nearest integer, ties to even, and leaves
+    // its two's complement in the low byte
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fminf(fmaxf(q[i], -127.f), 127.f) + 12582912.f);
+    r.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    r.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  } else {
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(q[2 * i + 1]), "f"(q[2 * i]));
+    r.x = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
+    r.y = static_cast<uint32_t>(h[2]) | (static_cast<uint32_t>(h[3]) << 16);
+  }
+  return r;
+}
+
+// One scaled value -> its code byte.
+template <int FMT>
+MDEV uint32_t act8_code(float q) {
+  if (FMT == METIS_MXINT8) return __float_as_uint(fminf(fmaxf(q, -127.f), 127.f) + 12582912.f) & 0xFFu;
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(q));
+  return h & 0xFFu;
+}
+
+// The factor of a block's elements: 2^(se - 6) or 2^se; NaN for code 255.
+// (A scale code below the codec's smallest has elements 0 only.)
+template <int FMT>
+MDEV float act8_factor(uint32_t sc) {
+  const uint32_t bits = FMT == METIS_MXINT8 ? (max(sc, 7u) - 6u) << 23 : sc << 23;
+  return __uint_as_float(sc == 255u ? 0x7FC00000u : bits);
+}
+
+// Element values (not yet scaled) of the 4 code bytes in w.
+template <int FMT>
+MDEV void act8_elems4(uint32_t w, float* v) {
+  if (FMT == METIS_MXINT8) {
+    // 2^23 + (code + 128) as a float, minus 2^23 + 128
+    const uint32_t u = w ^ 0x80808080u;
+    v[0] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650)) - 8388736.f;
+    v[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7651)) - 8388736.f;
+    v[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7652)) - 8388736.f;
+    v[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7653)) - 8388736.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h2;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w >> (16 * i))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// Element value (not yet scaled) of byte q of a word.
+template <int FMT>
+MDEV float act8_elem_at(uint32_t w, int q) {
+  if (FMT == METIS_MXINT8)
+    return __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4B000000u, 0x7650u + q)) - 8388736.f;
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w >> (8 * (q & 2)))));
+  const __half2 h = *reinterpret_cast<const __half2*>(&h2);
+  return (q & 1) ? __high2float(h) : __low2float(h);
+}
+
+template <int FMT>
+MDEV float act8_elem(uint32_t byte) {
+  if (FMT == METIS_MXINT8) return static_cast<float>(static_cast<int8_t>(byte));
+  float v[4];
+  act8_elems4<FMT>(byte, v);
+  return v[0];
+}
+
+// The largest magnitude a block with maximum a holds (rounding is monotonic);
+// 0 for a block that reads NaN.
+template <int FMT>
+MDEV float act8_block_amax(float a, float enc, uint32_t sc) {
+  const float m = act8_elem<FMT>(act8_code<FMT>(a * enc)) * act8_factor<FMT>(sc);
+  return sc == 255u ? 0.f : m;
+}
+
+// The calling CTA's maximum m (0 or more, valid in thread 0) into its slots of
+// the tensor's maximum: CTA b owns slots b, b + gridDim.x, ...; all but the
+// first hold 0.  gridDim.x <= METIS_ACT8_AMAX.
+MDEV void act8_write_amax(float* amax, float m) {
+  if (threadIdx.x != 0) return;
+  for (int i = blockIdx.x; i < METIS_ACT8_AMAX; i += gridDim.x) {
+    amax[i] = m;
+    m = 0.f;
+  }
+}
+
+}  // namespace metis
