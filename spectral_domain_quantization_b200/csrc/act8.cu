@@ -8,6 +8,7 @@
 #include "act8.cuh"
 #include "act8.h"
 #include "fp4_block.cuh"
+#include "rows.cuh"
 
 namespace metis {
 
@@ -15,35 +16,37 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// unit -> (row, unit in the row), by a 32-bit division where the count allows
+// unit -> (row, unit in the row): a multiplication by a rounded-up reciprocal
+// for fewer than 2^31 units (Granlund and Montgomery's division by an invariant:
+// with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (mulhi(n, m) + n) >> s), a 64-bit division otherwise.
 struct UnitMap {
   int64_t total;
   int64_t per_row;
+  uint32_t m, s;
   bool narrow;
-  MDEV void split(int64_t u, int64_t& row, int64_t& k) const {
+  MDEV void split(int64_t u, int64_t& row, int& k) const {
     if (narrow) {
-      const uint32_t r = static_cast<uint32_t>(u) / static_cast<uint32_t>(per_row);
+      const uint32_t n = static_cast<uint32_t>(u);
+      const uint32_t r = (__umulhi(n, m) + n) >> s;
       row = r;
-      k = static_cast<uint32_t>(u) - r * static_cast<uint32_t>(per_row);
+      k = static_cast<int>(n - r * static_cast<uint32_t>(per_row));
     } else {
       row = u / per_row;
-      k = u - row * per_row;
+      k = static_cast<int>(u - row * per_row);
     }
   }
 };
 
 UnitMap unit_map(int64_t rows, int64_t per_row) {
-  UnitMap m;
+  UnitMap m{};
   m.per_row = per_row;
   m.total = rows * per_row;
   m.narrow = m.total < (int64_t{1} << 31);
+  while ((int64_t{1} << m.s) < per_row) ++m.s;
+  m.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << m.s) - per_row)) / per_row + 1);
   return m;
 }
-
-MDEV float load1(const float* p) { return *p; }
-MDEV float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-MDEV void store1(float* p, float v) { *p = v; }
-MDEV void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 MDEV float cta_max(float m) {
   __shared__ float wm[kThreads / 32];
@@ -57,246 +60,142 @@ MDEV float cta_max(float m) {
   return m;
 }
 
-// 8 elements a thread, a block in 4 adjacent lanes (16-byte aligned rows):
-// loads of 16 bytes, code stores of 8, both contiguous over the warp.
-template <int FMT, typename T>
-__global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t cols, int64_t ld, Act8View out,
-                                                             UnitMap map) {
-  constexpr int kU = 4;                          // units in flight per thread
-  constexpr int kWords = sizeof(T) == 2 ? 1 : 2;  // 16-byte words of a unit
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  float top = 0.f;
-  // a multiple of 32 units per step: the loop's bound is the same for a warp
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - (threadIdx.x & 31) < map.total;
-       u0 += kU * stride) {
-    uint4 raw[kU][kWords];
-    int64_t row[kU], k[kU];
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int64_t u = u0 + i * stride;
-      row[i] = k[i] = 0;
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) raw[i][w] = make_uint4(0, 0, 0, 0);
-      if (u < map.total) {
-        map.split(u, row[i], k[i]);
-        const T* src = X + row[i] * ld + 8 * k[i];
-        const int64_t left = cols - 8 * k[i];
-        if (left >= 8) {
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) raw[i][w] = __ldcs(reinterpret_cast<const uint4*>(src) + w);
-        } else {
-          T* e = reinterpret_cast<T*>(raw[i]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < left) e[j] = src[j];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int64_t u = u0 + i * stride;
-      float v[8];
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        const uint32_t x[4] = {raw[i][w].x, raw[i][w].y, raw[i][w].z, raw[i][w].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (sizeof(T) == 2) {
-            v[2 * j] = __uint_as_float(x[j] << 16);
-            v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-          } else {
-            v[4 * w + j] = __uint_as_float(x[j]);
-          }
-        }
-      }
-      float a = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a = max_nan(a, fabsf(v[j]));
-      a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-      a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-      if (u < map.total) {
-        float enc;
-        const uint32_t sc = act8_scale<FMT>(a, enc);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= enc;
-        uint2 codes = act8_pack8<FMT>(v);
-        if (sc == 255u) codes = make_uint2(0u, 0u);
-        __stcs(reinterpret_cast<uint2*>(out.codes + row[i] * out.ldc + 8 * k[i]), codes);
-        if ((k[i] & 3) == 0) out.scales[row[i] * out.blocks + (k[i] >> 2)] = static_cast<uint8_t>(sc);
-        top = fmaxf(top, act8_block_amax<FMT>(a, enc, sc));
-      }
-    }
-  }
-  act8_write_amax(out.amax, cta_max(top));
-}
-
-// One column a lane, a block a warp: rows that start anywhere.
-template <int FMT, typename T>
-__global__ void __launch_bounds__(kThreads) act8_save_any_kernel(const T* X, int64_t cols, int64_t ld, Act8View out,
-                                                                 UnitMap map) {
-  constexpr int kU = 8;
+// 8 elements a thread, a block in 4 adjacent lanes.  The units of all rows form
+// one sequence (a row's are a multiple of 4), dealt to the lanes in order.
+template <int FMT, typename T, bool AL>
+__global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t rows, int64_t cols, int64_t ld,
+                                                             Act8View out, UnitMap map) {
+  constexpr int kU = sizeof(T) == 2 ? 4 : 2;      // units in flight per thread
   const int lane = threadIdx.x & 31;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  const Span span = span_of<T>(X, rows, cols, ld);
   float top = 0.f;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u0 < map.total;
+  // the loop's bound is the same for a warp
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
        u0 += kU * stride) {
-    float v[kU];
-    int64_t row[kU], k[kU];
+    UnitLoad<T, AL> in[kU];
+    int64_t row[kU];
+    int k[kU], left[kU];
+    bool last[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int64_t u = u0 + i * stride;
-      v[i] = 0.f;
-      row[i] = k[i] = 0;
+      row[i] = 0;
+      k[i] = 0;
+      left[i] = -16;
       if (u < map.total) {
         map.split(u, row[i], k[i]);
-        const int64_t c = 32 * k[i] + lane;
-        if (c < cols) v[i] = load1(X + row[i] * ld + c);
+        left[i] = static_cast<int>(cols) - 8 * k[i];
       }
+      last[i] = lane == 31 || k[i] + 1 == map.per_row;
+      in[i].start(X + row[i] * ld + 8 * k[i], left[i], last[i], span);
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      if (u0 + i * stride >= map.total) break;   // the same for the whole warp
-      // the bits of |x| order like the values, with NaN above infinity
-      const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[i]) & 0x7FFFFFFFu));
-      float enc;
-      const uint32_t sc = act8_scale<FMT>(a, enc);
-      uint32_t code = act8_code<FMT>(v[i] * enc);
-      if (sc == 255u) code = 0u;
-      out.codes[row[i] * out.ldc + 32 * k[i] + lane] = static_cast<uint8_t>(code);
-      if (lane == 0) out.scales[row[i] * out.blocks + k[i]] = static_cast<uint8_t>(sc);
-      top = fmaxf(top, act8_block_amax<FMT>(a, enc, sc));
+      const bool mine = u0 + i * stride < map.total;
+      const Unit<T> x = in[i].finish(left[i], last[i]);
+      float v[8];
+      x.get(v);
+      uint32_t codes[2];
+      const uint32_t sc = act8_block<FMT, 8>(v, codes, top);
+      if (mine) {
+        *reinterpret_cast<uint2*>(out.codes + row[i] * out.ldc + 8 * k[i]) = make_uint2(codes[0], codes[1]);
+        if ((k[i] & 3) == 0) out.scales[row[i] * out.blocks + (k[i] >> 2)] = static_cast<uint8_t>(sc);
+      }
     }
   }
-  act8_write_amax(out.amax, cta_max(top));
+  act8_write_amax(out.amax, act8_held<FMT>(cta_max(top)));
 }
 
-// 16 elements a thread (16-byte loads of codes), 16-byte aligned output rows.
-template <int FMT, typename T>
+// 8 elements a thread, as in act8_save_kernel; a row's units stop at its last
+// column.
+template <int FMT, typename T, bool AL>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View in, int64_t cols, T* Y, int64_t ld,
                                                                 UnitMap map) {
   constexpr int kU = 4;
+  const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 < map.total; u0 += kU * stride) {
-    uint4 raw[kU];
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
+       u0 += kU * stride) {
+    uint2 raw[kU];
     uint32_t sc[kU];
-    int64_t row[kU], k[kU];
+    int64_t row[kU];
+    int k[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int64_t u = u0 + i * stride;
-      row[i] = k[i] = 0;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      sc[i] = 0;
+      row[i] = 0;
+      k[i] = 0;
+      raw[i] = make_uint2(0u, 0u);
+      sc[i] = 0u;
       if (u < map.total) {
         map.split(u, row[i], k[i]);
-        raw[i] = __ldcs(reinterpret_cast<const uint4*>(in.codes + row[i] * in.ldc) + k[i]);
-        sc[i] = in.scales[row[i] * in.blocks + (k[i] >> 1)];
+        raw[i] = *reinterpret_cast<const uint2*>(in.codes + row[i] * in.ldc + 8 * k[i]);
+        sc[i] = in.scales[row[i] * in.blocks + (k[i] >> 2)];
       }
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      if (u0 + i * stride >= map.total) continue;
       const float f = act8_factor<FMT>(sc[i]);
-      float v[16];
+      float v[8];
       act8_elems4<FMT>(raw[i].x, v);
       act8_elems4<FMT>(raw[i].y, v + 4);
-      act8_elems4<FMT>(raw[i].z, v + 8);
-      act8_elems4<FMT>(raw[i].w, v + 12);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] *= f;
-      T* dst = Y + row[i] * ld + 16 * k[i];
-      const int64_t left = cols - 16 * k[i];
-      if (left >= 16) {
-        if constexpr (sizeof(T) == 2) {
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-          __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            __stcs(reinterpret_cast<float4*>(dst) + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < left) store1(dst + j, v[j]);
-      }
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+      Unit<T> y;
+      y.put(v);
+      const int left = u0 + i * stride < map.total ? static_cast<int>(cols) - 8 * k[i] : 0;
+      store_unit<T, AL>(Y + row[i] * ld + 8 * k[i], y, left, lane == 0 || k[i] == 0,
+                        lane == 31 || k[i] + 1 == map.per_row);
     }
   }
 }
 
-// One column a lane, a block a warp: output rows that start anywhere.
-template <int FMT, typename T>
-__global__ void __launch_bounds__(kThreads) act8_restore_any_kernel(Act8View in, int64_t cols, T* Y, int64_t ld,
-                                                                    UnitMap map) {
-  constexpr int kU = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u0 < map.total;
-       u0 += kU * stride) {
-    uint32_t code[kU], sc[kU];
-    int64_t row[kU], k[kU];
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int64_t u = u0 + i * stride;
-      code[i] = sc[i] = 0;
-      row[i] = k[i] = 0;
-      if (u < map.total) {
-        map.split(u, row[i], k[i]);
-        code[i] = in.codes[row[i] * in.ldc + 32 * k[i] + lane];
-        sc[i] = in.scales[row[i] * in.blocks + k[i]];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int64_t c = 32 * k[i] + lane;
-      if (u0 + i * stride < map.total && c < cols)
-        store1(Y + row[i] * ld + c, act8_elem<FMT>(code[i]) * act8_factor<FMT>(sc[i]));
-    }
-  }
-}
-
-int grid_for(const void* kernel, int64_t ctas, int num_sms) {
-  // no more CTAs than are resident at once: the loops are grid-strided
+int occupancy(const void* kernel) {
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) != cudaSuccess || per_sm < 1)
     per_sm = 1;
+  return per_sm;
+}
+
+// no more CTAs than are resident at once: the loops are grid-strided
+int grid_for(int per_sm, int64_t ctas, int num_sms) {
   const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX);
   return static_cast<int>(imax64(1, imin64(ctas, most)));
 }
 
+template <int FMT, typename T, bool AL>
+void save_al(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
+  const UnitMap map = unit_map(rows, 4 * out.blocks);
+  auto* kernel = act8_save_kernel<FMT, T, AL>;
+  static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
+  kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(X, rows, cols, ld, out,
+                                                                                             map);
+}
+
+template <int FMT, typename T, bool AL>
+void restore_al(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
+  const UnitMap map = unit_map(rows, (cols + 7) / 8);
+  auto* kernel = act8_restore_kernel<FMT, T, AL>;
+  static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
+  kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(in, cols, Y, ld, map);
+}
+
+template <typename T>
+bool aligned_rows(const T* p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
+}
+
 template <int FMT, typename T>
 void save_t(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
-  if ((reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0) {
-    const UnitMap map = unit_map(rows, 4 * out.blocks);
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_save_kernel<FMT, T>),
-                              (map.total + kThreads - 1) / kThreads, num_sms);
-    act8_save_kernel<FMT, T><<<grid, kThreads, 0, s>>>(X, cols, ld, out, map);
-  } else {
-    const UnitMap map = unit_map(rows, out.blocks);
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_save_any_kernel<FMT, T>),
-                              (map.total + kThreads / 32 - 1) / (kThreads / 32), num_sms);
-    act8_save_any_kernel<FMT, T><<<grid, kThreads, 0, s>>>(X, cols, ld, out, map);
-  }
+  aligned_rows(X, ld) ? save_al<FMT, T, true>(X, rows, cols, ld, out, num_sms, s)
+                      : save_al<FMT, T, false>(X, rows, cols, ld, out, num_sms, s);
 }
 
 template <int FMT, typename T>
 void restore_t(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
-  if ((reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0) {
-    const UnitMap map = unit_map(rows, (cols + 15) / 16);
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_restore_kernel<FMT, T>),
-                              (map.total + kThreads - 1) / kThreads, num_sms);
-    act8_restore_kernel<FMT, T><<<grid, kThreads, 0, s>>>(in, cols, Y, ld, map);
-  } else {
-    const UnitMap map = unit_map(rows, in.blocks);
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_restore_any_kernel<FMT, T>),
-                              (map.total + kThreads / 32 - 1) / (kThreads / 32), num_sms);
-    act8_restore_any_kernel<FMT, T><<<grid, kThreads, 0, s>>>(in, cols, Y, ld, map);
-  }
+  aligned_rows(Y, ld) ? restore_al<FMT, T, true>(in, rows, cols, Y, ld, num_sms, s)
+                      : restore_al<FMT, T, false>(in, rows, cols, Y, ld, num_sms, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -471,11 +370,11 @@ template <int FMT8, int FMT4>
 void quantize_t(const Act8QuantParams& p, int axis, int num_sms, cudaStream_t s) {
   const int64_t tiles = p.otiles * p.itiles;
   if (axis == 1) {
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 1>), tiles, num_sms);
-    act8_quantize_kernel<FMT8, FMT4, 1><<<grid, kThreads, 0, s>>>(p);
+    static const int per_sm = occupancy(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 1>));
+    act8_quantize_kernel<FMT8, FMT4, 1><<<grid_for(per_sm, tiles, num_sms), kThreads, 0, s>>>(p);
   } else {
-    const int grid = grid_for(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 0>), tiles, num_sms);
-    act8_quantize_kernel<FMT8, FMT4, 0><<<grid, kThreads, 0, s>>>(p);
+    static const int per_sm = occupancy(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 0>));
+    act8_quantize_kernel<FMT8, FMT4, 0><<<grid_for(per_sm, tiles, num_sms), kThreads, 0, s>>>(p);
   }
 }
 

@@ -38,27 +38,50 @@ MDEV uint32_t act8_scale(float a, float& enc) {
   return a == 0.f ? 0u : static_cast<uint32_t>(se + 127);
 }
 
-// 8 scaled values (x enc) -> 8 code bytes, element i in byte i.
+// 4 scaled values (x enc) -> 4 code bytes, element i in byte i.  `clamp`: the
+// block's maximum rounds to 128 (MXINT8); without it no value does.
 template <int FMT>
-MDEV uint2 act8_pack8(const float* q) {
-  uint2 r;
+MDEV uint32_t act8_pack4(const float* q, bool clamp) {
   if (FMT == METIS_MXINT8) {
     // 1.5 2^23 + q rounds q to the nearest integer, ties to even, and leaves
     // its two's complement in the low byte
-    uint32_t b[8];
+    uint32_t b[4];
+    if (clamp) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fminf(fmaxf(q[i], -127.f), 127.f) + 12582912.f);
-    r.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    r.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-  } else {
-    uint16_t h[4];
+      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fminf(fmaxf(q[i], -127.f), 127.f) + 12582912.f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(q[2 * i + 1]), "f"(q[2 * i]));
-    r.x = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
-    r.y = static_cast<uint32_t>(h[2]) | (static_cast<uint32_t>(h[3]) << 16);
+      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + 12582912.f);
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
-  return r;
+  uint16_t h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(q[2 * i + 1]), "f"(q[2 * i]));
+  return static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
+}
+
+// A block whose 32 columns lie in 32 / E adjacent lanes, E each (by whole warps):
+// this lane's codes and the scale code.  `top` follows the largest finite
+// maximum; what 8 bits hold of it is the tensor's largest magnitude, since the
+// rounding of a block's maximum grows with the maximum.
+template <int FMT, int E>
+MDEV uint32_t act8_block(const float* v, uint32_t* codes, float& top) {
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j) a = max_nan(a, fabsf(v[j]));
+#pragma unroll
+  for (int off = 1; off < 32 / E; off <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
+  float enc, q[E];
+  const uint32_t sc = act8_scale<FMT>(a, enc);
+#pragma unroll
+  for (int j = 0; j < E; ++j) q[j] = v[j] * enc;
+  const bool clamp = a * enc > 127.f;
+#pragma unroll
+  for (int k = 0; k < E / 4; ++k) codes[k] = sc == 255u ? 0u : act8_pack4<FMT>(q + 4 * k, clamp);
+  if (sc != 255u) top = fmaxf(top, a);
+  return sc;
 }
 
 // One scaled value -> its code byte.
@@ -119,12 +142,12 @@ MDEV float act8_elem(uint32_t byte) {
   return v[0];
 }
 
-// The largest magnitude a block with maximum a holds (rounding is monotonic);
-// 0 for a block that reads NaN.
+// The largest magnitude held of blocks whose largest finite maximum is a.
 template <int FMT>
-MDEV float act8_block_amax(float a, float enc, uint32_t sc) {
-  const float m = act8_elem<FMT>(act8_code<FMT>(a * enc)) * act8_factor<FMT>(sc);
-  return sc == 255u ? 0.f : m;
+MDEV float act8_held(float a) {
+  float enc;
+  const uint32_t sc = act8_scale<FMT>(a, enc);
+  return act8_elem<FMT>(act8_code<FMT>(a * enc)) * act8_factor<FMT>(sc);
 }
 
 // The calling CTA's maximum m (0 or more, valid in thread 0) into its slots of

@@ -1,257 +1,250 @@
-// What the layer norm's forward and backward kernels share: how a row is spread
-// over threads, its loads and stores, and the sums over a row.
+// What the layer norm's forward and backward kernels share: how rows are spread
+// over threads, and the sums over a row.
 //
 // A row is held in registers by G threads: part of a warp, a warp, a CTA, or a
 // cluster of CTAs that take a slice of the columns each (sums meet in
-// distributed shared memory).  Each thread has NV units of 8 columns:
-//   VEC == 8: 8 consecutive columns a unit (rows on 16-byte boundaries), so a
-//             warp's loads and stores are 16 bytes a lane;
-//   VEC == 1: the unit's columns G apart, one element a lane (rows that start
-//             anywhere: a warp still touches contiguous bytes).
+// distributed shared memory).  Each thread has NV units of E consecutive columns
+// (rows.cuh), the same columns in every row: 32 columns a thread, so what a row
+// costs besides its elements (reductions, roots, addresses) is spread over many.
+// E is 8 where every matrix is bf16 (16-byte words) and 4 where one is float32, so
+// that a warp's words are contiguous.  The rows to come wait in a ring in shared
+// memory.
 #pragma once
+
+#include <atomic>
+#include <type_traits>
 
 #include "act8.cuh"
 #include "layer_norm.h"
+#include "rows.cuh"
 
 namespace metis {
 
 template <int G>
 constexpr int norm_threads() {
-  return G >= 128 ? G : 128;
+  return G >= 64 ? G : 128;
 }
 
-MDEV float load_any(const void* p, int dtype, int64_t i) { return load_elem(p, dtype, i); }
-
-MDEV void unpack8(const uint4& u, float* v) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-MDEV uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-MDEV void store_any(void* p, int dtype, int64_t i, float v) {
-  if (dtype == METIS_BF16)
-    reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else
-    reinterpret_cast<float*>(p)[i] = v;
-}
-
-// 8 values to 8 consecutive elements; n < 8 of them where the row ends.
-MDEV void store_unit(void* p, int dtype, int64_t i, const float* v, int n) {
-  if (n >= 8) {
-    if (dtype == METIS_BF16) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + i) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
-    } else {
-      float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-      d[0] = make_float4(v[0], v[1], v[2], v[3]);
-      d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) store_any(p, dtype, i + j, v[j]);
-  }
-}
-
-// The columns of one thread.
-template <int G, int NV, int VEC, bool CL>
+// The columns and rows of one thread.
+template <int G, int NV, int E, int MODE, bool CL>
 struct NormCols {
-  int begin, end;   // this CTA's columns
+  static constexpr int kSpan = G < 32 ? G : 32;   // lanes of one row in a warp
+  static constexpr int kThreads = norm_threads<G>();
+  static constexpr int kRows = kThreads / G;      // rows a CTA has at once
+  int lo, hi;       // this CTA's columns
+  int c0;           // this thread's first column (kPhase: may be outside)
   int t;            // thread within the row's threads of this CTA
-  MDEV NormCols(int cols, int slice) {
+  bool first, last; // lane of the row's lanes in the warp
+  int64_t row, step;  // first row, and from one to the next
+
+  // `period`, `ld`, `offset` (kPhase): row r's first element is (offset + r ld) mod
+  // `width` elements behind a period's begin; that of rows `period` apart is equal
+  MDEV NormCols(int cols, int slice, int ctas, int period, int64_t ld, int offset, int width) {
     t = static_cast<int>(threadIdx.x) % G;
-    begin = CL ? static_cast<int>(cluster_rank()) * slice : 0;
-    end = CL ? min(cols, begin + slice) : cols;
+    first = t % kSpan == 0;
+    last = t % kSpan == kSpan - 1;
+    const int64_t blocks = CL ? gridDim.x / ctas : gridDim.x;
+    const int64_t group = static_cast<int64_t>(CL ? blockIdx.x / ctas : blockIdx.x) * kRows + threadIdx.x / G;
+    int shift = 0;
+    row = group;
+    step = blocks * kRows;                // a multiple of the period
+    if constexpr (MODE == kPhase) shift = static_cast<int>((offset + row * ld) & (width - 1));
+    const int begin = CL ? static_cast<int>(cluster_rank()) * slice - shift : -shift;
+    c0 = begin + t * E;
+    lo = max(begin, 0);
+    hi = CL ? min(cols, begin + slice) : cols;
   }
-  MDEV int col(int i, int j) const { return VEC == 8 ? begin + (i * G + t) * 8 + j : begin + (i * 8 + j) * G + t; }
-  // how many of unit i's columns exist (VEC == 8)
-  MDEV int left(int i) const { return end - (begin + (i * G + t) * 8); }
-  MDEV bool has(int i, int j) const { return col(i, j) < end; }
+  MDEV int col(int i) const { return c0 + i * (G * E); }
+  MDEV int left(int i) const { return hi - col(i); }      // columns from unit i's first on
+  MDEV bool some(int i) const { return MODE == kPhase ? col(i) < hi && col(i) + E > lo : col(i) < hi; }
+  MDEV bool whole(int i) const {
+    return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? col(i) >= lo && col(i) + E <= hi : col(i) + E <= hi);
+  }
+  MDEV bool has(int i, int j) const { return col(i) + j < hi && (MODE != kPhase || col(i) + j >= lo); }
 };
 
 // Per-column vector (weight or bias) into registers; `none` where it is absent.
-template <int G, int NV, int VEC, bool CL>
-MDEV void load_vector(const NormCols<G, NV, VEC, CL>& cs, const void* p, int dtype, float none, float* out) {
+template <int G, int NV, int E, int MODE, bool CL>
+MDEV void load_vector(const NormCols<G, NV, E, MODE, CL>& cs, const void* p, int dtype, float none, float* out) {
   if (!p) {
 #pragma unroll
-    for (int k = 0; k < NV * 8; ++k) out[k] = none;
+    for (int k = 0; k < NV * E; ++k) out[k] = none;
     return;
   }
-  const bool wide = VEC == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+  if (MODE == kAligned && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (wide && cs.left(i) >= 8) {
+    for (int i = 0; i < NV; ++i) {
+      const int c = cs.some(i) ? cs.col(i) : 0;     // (the columns are a multiple of E)
       if (dtype == METIS_BF16) {
-        unpack8(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + cs.col(i, 0)), out + 8 * i);
+        Unit<__nv_bfloat16, E> u;
+        const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
+#pragma unroll
+        for (int k = 0; k < E / 4; ++k) {
+          const uint2 x = q[k];
+          u.w[2 * k] = x.x;
+          u.w[2 * k + 1] = x.y;
+        }
+        u.get(out + E * i);
       } else {
-        const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + cs.col(i, 0));
-        const float4 a = q[0], b = q[1];
-        out[8 * i] = a.x; out[8 * i + 1] = a.y; out[8 * i + 2] = a.z; out[8 * i + 3] = a.w;
-        out[8 * i + 4] = b.x; out[8 * i + 5] = b.y; out[8 * i + 6] = b.z; out[8 * i + 7] = b.w;
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+#pragma unroll
+        for (int k = 0; k < E / 4; ++k) {
+          const float4 x = q[k];
+          out[E * i + 4 * k] = x.x;
+          out[E * i + 4 * k + 1] = x.y;
+          out[E * i + 4 * k + 2] = x.z;
+          out[E * i + 4 * k + 3] = x.w;
+        }
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) out[8 * i + j] = cs.has(i, j) ? load_any(p, dtype, cs.col(i, j)) : 0.f;
     }
-  }
-}
-
-// One unit of a dense row, as loaded.
-template <typename T, int VEC>
-struct RawUnit;
-
-template <>
-struct RawUnit<__nv_bfloat16, 8> {
-  uint4 q;
-  MDEV void zero() { q = make_uint4(0, 0, 0, 0); }
-  MDEV void load(const __nv_bfloat16* p, int n) {
-    if (n >= 8) {
-      q = *reinterpret_cast<const uint4*>(p);
-    } else {
-      zero();
-      uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) w[j >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[j])) << (16 * (j & 1));
-      q = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  MDEV void get(float* v) const { unpack8(q, v); }
-};
-
-template <>
-struct RawUnit<float, 8> {
-  float4 a, b;
-  MDEV void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  MDEV void load(const float* p, int n) {
-    if (n >= 8) {
-      a = *reinterpret_cast<const float4*>(p);
-      b = *reinterpret_cast<const float4*>(p + 4);
-    } else {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.f;
-      a = make_float4(v[0], v[1], v[2], v[3]);
-      b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  }
-  MDEV void get(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-};
-
-template <typename T>
-struct RawUnit<T, 1> {
-  T e[8];
-  MDEV void zero() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = static_cast<T>(0.f);
-  }
-  MDEV void get(float* v) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(e[j]);
-  }
-};
-
-// Unit i of the row at `p`.
-template <typename T, int G, int NV, int VEC, bool CL>
-MDEV void load_row_unit(const NormCols<G, NV, VEC, CL>& cs, const T* p, int i, bool active, RawUnit<T, VEC>& r) {
-  if constexpr (VEC == 8) {
-    const int n = cs.left(i);
-    if (active && n > 0)
-      r.load(p + cs.col(i, 0), n);
-    else
-      r.zero();
   } else {
-    r.zero();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (active && cs.has(i, j)) r.e[j] = p[cs.col(i, j)];
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < E; ++j) out[E * i + j] = cs.has(i, j) ? load_any(p, dtype, cs.col(i) + j) : 0.f;
   }
 }
 
-// Sums of two values over a row, the same in all its threads.  Two buffers in
-// turn: a buffer is written again only after every thread has passed the
-// barrier that follows its last reading.
-template <int G, bool CL>
-struct RowSum {
+// Unit i of an output row of type TY at `p` (its first column's place).
+template <typename TY, int G, int NV, int E, int MODE, bool CL>
+MDEV void store_row_unit(const NormCols<G, NV, E, MODE, CL>& cs, TY* p, const float* v, int i, bool active) {
+  if constexpr (MODE == kAny) {
+    Unit<TY> u;
+    u.put(v);
+    store_unit<TY, false>(p, u, active ? cs.left(i) : 0, cs.first, cs.last);
+  } else {
+    Unit<TY, E> u;
+    u.put(v);
+    if (active && cs.whole(i)) {
+      u.store(p);
+    } else if (MODE == kPhase && active && cs.some(i)) {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (cs.has(i, j)) p[j] = u.elem(j);
+    }
+  }
+}
+
+// y: the row's place of column 0, in bytes.
+template <int G, int NV, int E, int MODE, bool CL>
+MDEV void store_row_unit_any(const NormCols<G, NV, E, MODE, CL>& cs, void* y, int dtype, const float* v, int i,
+                             bool active) {
+  if (dtype == METIS_BF16)
+    store_row_unit(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
+  else
+    store_row_unit(cs, static_cast<float*>(y) + cs.col(i), v, i, active);
+}
+
+// s / n for n's rounded reciprocal: one correction of the product (Markstein),
+// correctly rounded as long as nothing overflows or underflows.
+MDEV float divide(float s, float n, float inv) {
+  const float q = s * inv;
+  const float r = fmaf(fmaf(-q, n, s), inv, q);
+  return fabsf(q) < 3e38f ? r : q;       // keeps infinities and NaN
+}
+
+// 1 / sqrt(a), the hardware's approximation and one Newton step.
+MDEV float inv_sqrt(float a) {
+  const float y = rsqrtf(a);
+  const float e = fmaf(-a * y, y, 1.f);
+  return fabsf(e) < 0.5f ? fmaf(0.5f * y, e, y) : y;   // a of 0, infinity or NaN: as it is
+}
+
+// Sum of N values (a power of two) in a balanced tree: a value passes through
+// log2 N additions, so an outlier does not cost the values after it their bits.
+template <int N>
+MDEV float tree_sum(const float* v) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    return tree_sum<N / 2>(v) + tree_sum<N / 2>(v + N / 2);
+  }
+}
+
+// Sums over a warp of two values at once: in the first step a lane passes on the
+// one it does not keep.  Lanes 0 to 15 end with the sum of a, the others with b's.
+MDEV float warp_sums2(float a, float b) {
+  const bool hi = threadIdx.x & 16;
+  float x = (hi ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, 16);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
+
+// Sum over groups of `span` (a power of two) adjacent lanes, in all of them.
+template <int kSpan>
+MDEV float span_sum(float x) {
+#pragma unroll
+  for (int off = kSpan / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
+
+// Sum over a CTA of 1024 threads, in all of them.
+MDEV float cta_sum(float x, float* buf) {
+  x = span_sum<32>(x);
+  __syncthreads();                      // the last call's sums have been read
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  return span_sum<32>(buf[threadIdx.x & 31]);
+}
+
+// V floats of every warp of a row's CTA or cluster, exchanged through shared
+// memory: put() (lanes that hold one), then sync(), then at().  Two buffers in
+// turn: a buffer is written again only after every thread has passed the barrier
+// that follows its last reading.
+template <int G, int V, bool CL>
+struct Exchange {
   static constexpr int kWarps = G / 32 > 0 ? G / 32 : 1;
-  static constexpr int kEntries = CL ? 8 * kWarps : kWarps;
-  float2* buf;      // shared memory, 2 * kEntries
+  static constexpr int kMost = (CL ? 4 : 1) * kWarps;    // warps of a row (a power of two)
+  static constexpr int kFloats = 2 * V * kMost;
+  float* buf;
+  int ctas;
   int phase = 0;
-  int ctas;         // CTAs of the cluster
-  MDEV RowSum(float2* b, int n) : buf(b), ctas(n) {}
-  MDEV float2 operator()(float x, float y) {
-    constexpr int kSpan = G < 32 ? G : 32;
-#pragma unroll
-    for (int off = kSpan / 2; off > 0; off >>= 1) {
-      x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-      y += __shfl_xor_sync(0xFFFFFFFFu, y, off);
-    }
-    if constexpr (G <= 32) {
-      return make_float2(x, y);
+  MDEV Exchange(float* b, int n) : buf(b), ctas(n) {}
+  MDEV int warps() const { return CL ? ctas * kWarps : kWarps; }
+  MDEV void put(int value, float x) {
+    const int warp = threadIdx.x >> 5;
+    float* b = buf + phase * (V * kMost) + value * kMost;
+    if constexpr (CL) {
+      // into every CTA of the cluster
+      const uint32_t at = smem_u32(b + static_cast<int>(cluster_rank()) * kWarps + warp);
+      for (int r = 0; r < ctas; ++r)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(at, static_cast<uint32_t>(r))), "f"(x)
+                     : "memory");
     } else {
-      float2* b = buf + phase * kEntries;
-      phase ^= 1;
-      const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kWarps;
-      float2 s = make_float2(0.f, 0.f);
-      if constexpr (CL) {
-        // every warp writes its sums into every CTA of the cluster
-        if (lane < ctas) {
-          const uint32_t dst =
-              map_to_rank(smem_u32(b + static_cast<int>(cluster_rank()) * kWarps + warp), static_cast<uint32_t>(lane));
-          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(x), "f"(y) : "memory");
-        }
-        cluster_sync_all();
-        const int n = ctas * kWarps;
-        for (int k = lane; k < n; k += 32) {
-          s.x += b[k].x;
-          s.y += b[k].y;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, off);
-          s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, off);
-        }
-      } else {
-        if (lane == 0) b[warp] = make_float2(x, y);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          s.x += b[k].x;
-          s.y += b[k].y;
-        }
-      }
-      return s;
+      b[warp] = x;
     }
+  }
+  MDEV const float* sync() {
+    const float* b = buf + phase * (V * kMost);
+    phase ^= 1;
+    if constexpr (CL)
+      cluster_sync_all();
+    else
+      __syncthreads();
+    return b;
   }
 };
 
-// Grid-wide: which block of rows' groups this CTA (or cluster) is.
-template <bool CL>
-MDEV int64_t norm_block(int ctas) {
-  return CL ? blockIdx.x / ctas : blockIdx.x;
-}
-
-inline int norm_cluster(int cols) { return cols <= 2 * 4096 ? 2 : (cols <= 4 * 4096 ? 4 : 8); }
+// Clusters: two CTAs of up to `per` columns each, or four.
+inline int norm_cluster(int cols, int per) { return cols <= 2 * per ? 2 : 4; }
 inline int norm_slice(int cols, int ctas) { return ((cols + ctas - 1) / ctas + 31) / 32 * 32; }
+
+// CTAs (or clusters) of `rows` groups each, up to `blocks` but so many that the
+// groups are a multiple of the rows' period.
+inline int64_t norm_blocks(int64_t blocks, int rows, int period) {
+  int64_t unit = 1;
+  while ((unit * rows) % period) ++unit;
+  return imax64(unit, blocks / unit * unit);
+}
 
 // Launch `kernel` on `grid` CTAs, in clusters of `ctas` where that is not 1.
 template <typename P>
-void norm_launch(void (*kernel)(P, int), int grid, int threads, int ctas, const P& p, cudaStream_t s) {
+void norm_launch(void (*kernel)(P, int), int grid, int threads, int smem, int ctas, const P& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -262,12 +255,53 @@ void norm_launch(void (*kernel)(P, int), int grid, int threads, int ctas, const 
   cudaLaunchKernelEx(&cfg, kernel, p, ctas);
 }
 
+// CTAs of `kernel` that an SM holds.  The limit of dynamic shared memory is an
+// attribute of the kernel on each device: `done` has a bit for every device it
+// was raised on.
 template <typename K>
-int norm_occupancy(K kernel, int threads) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess || per_sm < 1)
-    per_sm = 1;
-  return per_sm;
+int norm_occupancy(K kernel, int threads, int smem, std::atomic<uint64_t>& done, std::atomic<int>& per_sm) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+    per_sm.store(n, std::memory_order_relaxed);
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  return per_sm.load(std::memory_order_relaxed);
+}
+
+// A matrix of a call, for the choice of the kernels' row mode.
+struct RowsOf {
+  const void* p;
+  int64_t ld;
+  int dtype;
+};
+
+// The mode for matrices that are read and written together, and for kPhase the
+// rows' period and the first row's offset, in units of `width` elements.
+inline int norm_mode(const RowsOf* m, int count, int64_t cols, bool phase_ok, int width, int* period, int* offset) {
+  bool aligned = cols % 8 == 0, phase = phase_ok && cols + width - 1 <= kNormMaxCols;
+  int64_t off0 = 0, ld0 = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t es = m[i].dtype == METIS_BF16 ? 2 : 4;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(m[i].p);
+    aligned = aligned && a % 16 == 0 && (m[i].ld * es) % 16 == 0;
+    const int64_t off = static_cast<int64_t>((a / es) & (width - 1)), ld = m[i].ld & (width - 1);
+    if (i == 0) {
+      off0 = off;
+      ld0 = ld;
+    }
+    phase = phase && off == off0 && ld == ld0;
+  }
+  *period = 1;
+  *offset = static_cast<int>(off0);
+  if (aligned) return kAligned;
+  if (!phase) return kAny;
+  while ((*period * ld0) & (width - 1)) *period *= 2;
+  return kPhase;
 }
 
 }  // namespace metis

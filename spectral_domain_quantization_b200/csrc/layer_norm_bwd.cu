@@ -55,8 +55,7 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(NormBwdParams p
 
 // dx: a CTA a row, two passes over it.
 __global__ void __launch_bounds__(1024) norm_bwd_wide_rows_kernel(NormBwdParams p) {
-  __shared__ float2 sums[2 * RowSum<1024, false>::kEntries];
-  RowSum<1024, false> row_sum(sums, 1);
+  __shared__ float buf[32];
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float mean = p.mean[row], rstd = p.rstd[row];
     float s1 = 0.f, s2 = 0.f;
@@ -65,34 +64,42 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_rows_kernel(NormBwdParams 
       s1 = fmaf(g, (wide_x(p, row, c) - mean) * rstd, s1);
       s2 += g;
     }
-    const float2 t = row_sum(s1, s2);
-    const float c1 = t.x * p.inv_n, c2 = t.y * p.inv_n;
+    const float kd = -rstd * rstd * (cta_sum(s1, buf) * p.inv_n), k0 = -rstd * (cta_sum(s2, buf) * p.inv_n);
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
       const float g = load_any(p.dY, p.g_dtype, row * p.ldg + c) * (p.w ? load_any(p.w, p.w_dtype, c) : 1.f);
-      const float xh = (wide_x(p, row, c) - mean) * rstd;
-      store_any(p.dX, p.dx_dtype, row * p.ldd + c, rstd * fmaf(-xh, c1, g - c2));
+      store_any(p.dX, p.dx_dtype, row * p.ldd + c, fmaf(g, rstd, fmaf(wide_x(p, row, c) - mean, kd, k0)));
     }
   }
 }
 
-int dispatch(const NormBwdParams& p, int parts, bool occupancy, cudaStream_t s) {
-  if (!p.X) return norm_bwd_act8(p, parts, occupancy, s);
-  return p.x_dtype == METIS_BF16 ? norm_bwd_bf16(p, parts, occupancy, s) : norm_bwd_f32(p, parts, occupancy, s);
+int dispatch(const NormBwdParams& params, int parts, bool occupancy, int num_sms, cudaStream_t s) {
+  NormBwdParams p = params;
+  RowsOf m[3] = {{p.dY, p.ldg, p.g_dtype}};
+  int count = 1;
+  bool narrow = p.g_dtype == METIS_BF16;       // every matrix is bf16 (or 8 bits)
+  if (p.X) {
+    m[count++] = {p.X, p.ldx, p.x_dtype};
+    narrow = narrow && p.x_dtype == METIS_BF16;
+  }
+  if (p.dX) {
+    m[count++] = {p.dX, p.ldd, p.dx_dtype};
+    narrow = narrow && p.dx_dtype == METIS_BF16;
+  }
+  // the 8-bit blocks are columns of the matrix: no shift
+  const int mode = norm_mode(m, count, p.cols, p.X != nullptr, 8, &p.period, &p.offset);
+  if (!p.X) return norm_bwd_act8(p, mode, narrow, parts, occupancy, num_sms, s);
+  return p.x_dtype == METIS_BF16 ? norm_bwd_bf16(p, mode, narrow, parts, occupancy, num_sms, s)
+                                 : norm_bwd_f32(p, mode, narrow, parts, occupancy, num_sms, s);
 }
 
 }  // namespace
 
 int norm_bwd_parts(const NormBwdParams& p, int num_sms) {
   if (p.cols > kNormMaxCols) return static_cast<int>(imax64(1, imin64(p.rows, 16)));
-  const int r = dispatch(p, 0, true, nullptr);
-  const int at_once = r >> 16, per_sm = r & 0xFFFF;
-  const int ctas = p.cols > 4096 ? norm_cluster(p.cols) : 1;
-  const int64_t most = imax64(1, static_cast<int64_t>(num_sms) * per_sm / ctas);
-  return static_cast<int>(imax64(1, imin64((p.rows + at_once - 1) / at_once, most)));
+  return dispatch(p, 0, true, num_sms, nullptr);
 }
 
-void launch_norm_bwd(const NormBwdParams& params, int parts, cudaStream_t s) {
-  NormBwdParams p = params;
+void launch_norm_bwd(const NormBwdParams& p, int parts, cudaStream_t s) {
   if (p.cols > kNormMaxCols) {
     // the column sums first: dX may be dY
     if (p.part_w || p.part_b)
@@ -101,8 +108,7 @@ void launch_norm_bwd(const NormBwdParams& params, int parts, cudaStream_t s) {
     if (p.dX) norm_bwd_wide_rows_kernel<<<static_cast<unsigned>(imin64(p.rows, 296)), 1024, 0, s>>>(p);
     return;
   }
-  if (p.cols > 4096) p.slice = norm_slice(p.cols, norm_cluster(p.cols));
-  dispatch(p, parts, false, s);
+  dispatch(p, parts, false, 0, s);
 }
 
 void launch_norm_reduce(const float* part_w, const float* part_b, int parts, int64_t part_ld, int cols, float* dw,

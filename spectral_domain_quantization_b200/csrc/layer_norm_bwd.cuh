@@ -13,115 +13,197 @@
 
 namespace metis {
 
-// x of one unit: dense, or 8 codes and the block's factor.
 struct Act8Tag {};
 
-template <typename TX, int VEC>
-struct XUnit {
-  RawUnit<TX, VEC> r;
-  template <int G, int NV, bool CL>
-  MDEV void load(const NormCols<G, NV, VEC, CL>& cs, const NormBwdParams& p, int64_t row, int i, bool active) {
-    load_row_unit(cs, static_cast<const TX*>(p.X) + row * p.ldx, i, active, r);
-  }
-  MDEV void get(const NormBwdParams&, float* v) const { r.get(v); }
+// A unit of x in the ring: a dense one, or E codes of the 8-bit copy.
+template <typename TX, int E, int MODE, int kThreads, int kSpan>
+struct XSlot {
+  using Slot = UnitSlot<TX, E, MODE, kThreads, kSpan>;
+  static constexpr int kBytes = Slot::kBytes;
+};
+template <int E, int MODE, int kThreads, int kSpan>
+struct XSlot<Act8Tag, E, MODE, kThreads, kSpan> {
+  static constexpr int kBytes = E * kThreads;
 };
 
-template <>
-struct XUnit<Act8Tag, 8> {
-  uint2 q;
-  uint32_t sc;
-  template <int G, int NV, bool CL>
-  MDEV void load(const NormCols<G, NV, 8, CL>& cs, const NormBwdParams& p, int64_t row, int i, bool active) {
-    q = make_uint2(0u, 0u);
-    sc = 0u;
-    if (active && cs.left(i) > 0) {
-      const int c = cs.col(i, 0);
-      q = *reinterpret_cast<const uint2*>(p.saved.codes + row * p.saved.ldc + c);
-      sc = p.saved.scales[row * p.saved.blocks + (c >> 5)];
-    }
-  }
-  MDEV void get(const NormBwdParams& p, float* v) const {
+// x of one unit.
+template <typename TX, int E>
+struct XUnit {
+  Unit<TX, E> u;
+  MDEV void get(int, float* v) const { u.get(v); }
+};
+template <int E>
+struct XUnit<Act8Tag, E> {
+  uint32_t w[E / 4];
+  uint32_t sc;      // scale code
+  MDEV void get(int fmt, float* v) const {
     float f;
-    if (p.saved.fmt == METIS_MXINT8) {
+    if (fmt == METIS_MXINT8) {
       f = act8_factor<METIS_MXINT8>(sc);
-      act8_elems4<METIS_MXINT8>(q.x, v);
-      act8_elems4<METIS_MXINT8>(q.y, v + 4);
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXINT8>(w[k], v + 4 * k);
     } else {
       f = act8_factor<METIS_MXFP8>(sc);
-      act8_elems4<METIS_MXFP8>(q.x, v);
-      act8_elems4<METIS_MXFP8>(q.y, v + 4);
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXFP8>(w[k], v + 4 * k);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= f;
+    for (int j = 0; j < E; ++j) v[j] *= f;
   }
 };
 
+template <typename TX>
+struct DenseType {
+  using type = TX;
+};
 template <>
-struct XUnit<Act8Tag, 1> {
-  float e[8];
-  template <int G, int NV, bool CL>
-  MDEV void load(const NormCols<G, NV, 1, CL>& cs, const NormBwdParams& p, int64_t row, int i, bool active) {
-    uint32_t code[8], sc[8];
+struct DenseType<Act8Tag> {
+  using type = float;   // not used
+};
+
+template <typename TX, typename TG, int G, int NV, int E, int S, int MODE>
+struct BwdRing {
+  using C = NormCols<G, NV, E, MODE, false>;
+  using GS = UnitSlot<TG, E, MODE, C::kThreads, C::kSpan>;
+  using XS = XSlot<TX, E, MODE, C::kThreads, C::kSpan>;
+  static constexpr int kOne = GS::kBytes + XS::kBytes;
+  static constexpr int kStage = NV * kOne;
+  static constexpr int kGather = C::kRows > 1 ? C::kThreads * NV * E * 4 : 0;
+  static constexpr int kBytes = S * kStage > kGather ? S * kStage : kGather;
+};
+
+template <typename TX, typename TG, int G, int NV, int E, int S, int MODE, bool CL>
+__global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdParams p, int ctas) {
+  using Cols = NormCols<G, NV, E, MODE, CL>;
+  using Ring = BwdRing<TX, TG, G, NV, E, S, MODE>;
+  using GS = typename Ring::GS;
+  using DX = typename DenseType<TX>::type;
+  using XS = UnitSlot<DX, E, MODE, Cols::kThreads, Cols::kSpan>;   // dense x
+  using Ex = Exchange<G, 2, CL>;
+  constexpr bool kDense = !std::is_same_v<TX, Act8Tag>;
+  constexpr int kThreads = Cols::kThreads, kSpan = Cols::kSpan, kMost = Ex::kMost, kOwn = NV * E;
+  static_assert(kDense || MODE != kPhase, "the 8-bit blocks are columns of the matrix: no shift");
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float parts[Ex::kFloats];
+  const Cols cs(p.cols, p.slice, ctas, p.period, p.ldg, p.offset, 8);
+  Ex ex(parts, ctas);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const TG* dY = static_cast<const TG*>(p.dY);
+  const DX* X = static_cast<const DX*>(p.X);
+  const Span gspan = span_of<TG>(p.dY, p.rows, p.cols, p.ldg);
+  const Span xspan = span_of<DX>(p.X, p.rows, p.cols, p.ldx);
+  const uint32_t ring0 = smem_u32(ring);
+
+  // row `fetch_row` into the stage at `into`; what a row needs besides, its mean
+  // and rstd and the scale codes of its 8-bit blocks, goes into registers one row
+  // ahead
+  int64_t fetch_row = cs.row;
+  uint32_t into = ring0;
+  auto fetch = [&] {
+    const bool on = fetch_row < p.rows;
+    if (G < 32 || on) {
+      const TG* g = dY + fetch_row * p.ldg;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      code[j] = sc[j] = 0u;
-      if (active && cs.has(i, j)) {
-        const int c = cs.col(i, j);
-        code[j] = p.saved.codes[row * p.saved.ldc + c];
-        sc[j] = p.saved.scales[row * p.saved.blocks + (c >> 5)];
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t at = into + i * Ring::kOne;
+        if constexpr (MODE == kAny)
+          GS::start(at, tid, g + cs.col(i), on ? cs.left(i) : -16, cs.last, gspan);
+        else
+          GS::start(at, tid, g + cs.col(i), on && cs.whole(i), on && cs.some(i), gspan);
+        if constexpr (kDense) {
+          const DX* x = X + fetch_row * p.ldx;
+          if constexpr (MODE == kAny)
+            XS::start(at + GS::kBytes, tid, x + cs.col(i), on ? cs.left(i) : -16, cs.last, xspan);
+          else
+            XS::start(at + GS::kBytes, tid, x + cs.col(i), on && cs.whole(i), on && cs.some(i), xspan);
+        } else {
+          cp_async<E>(at + GS::kBytes + E * tid, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
+                      on && cs.left(i) > 0);
+        }
       }
     }
-    if (p.saved.fmt == METIS_MXINT8) {
+    cp_async_commit();
+    fetch_row += cs.step;
+    into = into + Ring::kStage == ring0 + S * Ring::kStage ? ring0 : into + Ring::kStage;
+  };
+  float next_mean = 0.f, next_rstd = 0.f;
+  uint32_t next_sc[kDense ? 1 : NV];
+  auto fetch_stats = [&](int64_t row) {
+    const bool on = row < p.rows;
+    next_mean = on ? p.mean[row] : 0.f;
+    next_rstd = on ? p.rstd[row] : 0.f;
+    if constexpr (!kDense) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = act8_elem<METIS_MXINT8>(code[j]) * act8_factor<METIS_MXINT8>(sc[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = act8_elem<METIS_MXFP8>(code[j]) * act8_factor<METIS_MXFP8>(sc[j]);
+      for (int i = 0; i < NV; ++i)
+        next_sc[i] = on && cs.left(i) > 0 ? p.saved.scales[row * p.saved.blocks + (cs.col(i) >> 5)] : 0u;
     }
-  }
-  MDEV void get(const NormBwdParams&, float* v) const {
+  };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e[j];
-  }
-};
-
-template <typename TX, typename TG, int G, int NV, int VEC, bool CL>
-__global__ void __launch_bounds__(norm_threads<G>(), G >= 256 ? 2 : 1) norm_bwd_kernel(NormBwdParams p, int ctas) {
-  constexpr int kThreads = norm_threads<G>();
-  constexpr int kRows = kThreads / G;
-  constexpr int kOwn = NV * 8;
-  __shared__ float2 sums[2 * RowSum<G, CL>::kEntries];
-  __shared__ float gather[kRows > 1 ? kThreads * kOwn : 1];
-  const NormCols<G, NV, VEC, CL> cs(p.cols, p.slice);
-  RowSum<G, CL> row_sum(sums, ctas);
-  const int g = static_cast<int>(threadIdx.x) / G;
-  const int64_t blk = norm_block<CL>(ctas);
-  const int64_t step = static_cast<int64_t>(CL ? gridDim.x / ctas : gridDim.x) * kRows;
-  if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
+  for (int k = 0; k < S - 1; ++k) fetch();
+  fetch_stats(cs.row);
   float w[kOwn], aw[kOwn], ab[kOwn];
   load_vector(cs, p.w, p.w_dtype, 1.f, w);
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) aw[k] = ab[k] = 0.f;
-  for (int64_t r0 = blk * kRows; r0 < p.rows; r0 += step) {
-    const int64_t row = r0 + g;
-    const bool active = row < p.rows;
-    XUnit<TX, VEC> xr[NV];
-    RawUnit<TG, VEC> gr[NV];
+  if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
+  uint32_t from = ring0;
+  // all threads of a row leave the loop together; with several rows in a warp,
+  // all of the warp
+  for (int64_t row = cs.row; G >= 32 ? row < p.rows : row - (lane / G) < p.rows; row += cs.step) {
+    fetch();
+    const bool active = G >= 32 || row < p.rows;
+    const float mean = next_mean, rstd = next_rstd;
+    uint32_t sc[kDense ? 1 : NV];
+    if constexpr (!kDense) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      load_row_unit(cs, static_cast<const TG*>(p.dY) + row * p.ldg, i, active, gr[i]);
-      xr[i].load(cs, p, row, i, active);
+      for (int i = 0; i < NV; ++i) sc[i] = next_sc[i];
     }
-    const float mean = active ? p.mean[row] : 0.f, rstd = active ? p.rstd[row] : 0.f;
-    float s1 = 0.f, s2 = 0.f;
+    fetch_stats(row + cs.step);
+    cp_async_wait<S - 1>();
+    auto g_unit = [&](int i) {
+      const uint32_t at = from + i * Ring::kOne;
+      if constexpr (MODE == kAny) {
+        return GS::finish(at, tid, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
+      } else {
+        Unit<TG, E> u = GS::finish(at, tid);
+        if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+        return u;
+      }
+    };
+    auto x_unit = [&](int i) {
+      const uint32_t at = from + i * Ring::kOne + GS::kBytes;
+      XUnit<TX, E> x;
+      if constexpr (!kDense) {
+        lds<E / 4>(at + E * tid, x.w);
+        x.sc = sc[i];
+      } else if constexpr (MODE == kAny) {
+        x.u = XS::finish(at, tid, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+      } else {
+        x.u = XS::finish(at, tid);
+        if (MODE == kPhase && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
+      }
+      return x;
+    };
+    // aligned units are read from the ring again for dx; those of rows that start
+    // anywhere are kept, since putting them together costs shuffles
+    constexpr bool kKeep = MODE == kAny;
+    XUnit<TX, E> xu[kKeep ? NV : 1];
+    Unit<TG, E> gu[kKeep ? NV : 1];
+    float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float x[8], dy[8];
-      xr[i].get(p, x);
-      gr[i].get(dy);
+      float x[E], dy[E];
+      const XUnit<TX, E> xv = x_unit(i);
+      const Unit<TG, E> gv = g_unit(i);
+      if constexpr (kKeep) {
+        xu[i] = xv;
+        gu[i] = gv;
+      }
+      xv.get(p.saved.fmt, x);
+      gv.get(dy);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = 8 * i + j;
+      for (int j = 0; j < E; ++j) {
+        const int k = E * i + j;
         const float xh = (x[j] - mean) * rstd, gk = dy[j] * w[k];
         s1 = fmaf(gk, xh, s1);
         s2 += gk;
@@ -130,107 +212,153 @@ __global__ void __launch_bounds__(norm_threads<G>(), G >= 256 ? 2 : 1) norm_bwd_
       }
     }
     if (p.dX) {
-      const float2 t = row_sum(s1, s2);
-      const float c1 = t.x * p.inv_n, c2 = t.y * p.inv_n;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float x[8], dy[8];
-        xr[i].get(p, x);
-        gr[i].get(dy);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = (x[j] - mean) * rstd;
-          dy[j] = rstd * (fmaf(-xh, c1, dy[j] * w[8 * i + j] - c2));
-        }
-        if constexpr (VEC == 8) {
-          const int n = cs.left(i);
-          if (active && n > 0) store_unit(p.dX, p.dx_dtype, row * p.ldd + cs.col(i, 0), dy, n);
+      float c1, c2;
+      if constexpr (G <= 32) {
+        c1 = span_sum<kSpan>(s1);
+        c2 = span_sum<kSpan>(s2);
+      } else {
+        const float s = warp_sums2(s1, s2);
+        if ((lane & 15) == 0) ex.put(lane >> 4, s);
+        const float* pt = ex.sync();
+        if constexpr (2 * kMost <= 32) {
+          const float t = span_sum<kMost>(lane % kMost < ex.warps() && lane < 2 * kMost ? pt[lane] : 0.f);
+          c1 = __shfl_sync(0xFFFFFFFFu, t, 0);
+          c2 = __shfl_sync(0xFFFFFFFFu, t, kMost);
         } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (active && cs.has(i, j)) store_any(p.dX, p.dx_dtype, row * p.ldd + cs.col(i, j), dy[j]);
+          float a = 0.f, b = 0.f;
+          for (int k = lane; k < ex.warps(); k += 32) {
+            a += pt[k];
+            b += pt[kMost + k];
+          }
+          c1 = span_sum<32>(a);
+          c2 = span_sum<32>(b);
         }
       }
+      // dx = rstd g + (x - mean) kd + k0
+      const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -rstd * (c2 * p.inv_n);
+      void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[E], dy[E];
+        if constexpr (kKeep) {
+          xu[i].get(p.saved.fmt, x);
+          gu[i].get(dy);
+        } else {
+          x_unit(i).get(p.saved.fmt, x);
+          g_unit(i).get(dy);
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, fmaf(x[j] - mean, kd, k0));
+        store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
+      }
     }
+    from = from + Ring::kStage == ring0 + S * Ring::kStage ? ring0 : from + Ring::kStage;
   }
-  // this CTA's partial sums
+  cp_async_wait<0>();
+  // this CTA's partial sums; the ring's memory is free
+  float* gather = reinterpret_cast<float*>(ring);
+  const int64_t blk = CL ? blockIdx.x / ctas : blockIdx.x;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float* part = which == 0 ? p.part_w : p.part_b;
     if (!part) continue;
     part += blk * p.part_ld;
     const float* a = which == 0 ? aw : ab;
-    if constexpr (kRows > 1) {
+    if constexpr (Cols::kRows > 1) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          gather[g * (G * kOwn) + cs.col(i, j)] = a[8 * i + j];
+        for (int j = 0; j < E; ++j)
+          if (cs.has(i, j)) gather[(tid / G) * (G * kOwn) + cs.col(i) + j] = a[E * i + j];
       __syncthreads();
-      for (int c = threadIdx.x; c < p.cols; c += kThreads) {
+      for (int c = tid; c < p.cols; c += kThreads) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) s += gather[k * (G * kOwn) + c];
+        for (int k = 0; k < Cols::kRows; ++k) s += gather[k * (G * kOwn) + c];
         part[c] = s;
       }
     } else {
-      const bool wide = VEC == 8 && (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
+      const bool wide = MODE != kPhase && (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (wide && cs.left(i) >= 8) {
-          float4* d = reinterpret_cast<float4*>(part + cs.col(i, 0));
-          d[0] = make_float4(a[8 * i], a[8 * i + 1], a[8 * i + 2], a[8 * i + 3]);
-          d[1] = make_float4(a[8 * i + 4], a[8 * i + 5], a[8 * i + 6], a[8 * i + 7]);
+        if (wide && cs.left(i) >= E) {
+#pragma unroll
+          for (int k = 0; k < E / 4; ++k)
+            reinterpret_cast<float4*>(part + cs.col(i))[k] =
+                make_float4(a[E * i + 4 * k], a[E * i + 4 * k + 1], a[E * i + 4 * k + 2], a[E * i + 4 * k + 3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (cs.has(i, j)) part[cs.col(i, j)] = a[8 * i + j];
+          for (int j = 0; j < E; ++j)
+            if (cs.has(i, j)) part[cs.col(i) + j] = a[E * i + j];
         }
       }
     }
   }
 }
 
-// Launches, or (occupancy) returns the CTAs an SM holds times the rows a CTA
-// has at once, as (rows << 16) | CTAs.
-template <typename TX, typename TG, int G, int NV, int VEC, bool CL>
-int norm_bwd_go(const NormBwdParams& p, int parts, bool occupancy, cudaStream_t s) {
-  constexpr int kThreads = norm_threads<G>();
-  auto* kernel = norm_bwd_kernel<TX, TG, G, NV, VEC, CL>;
+constexpr int kWideBwdCta = 256 * 32;      // columns of a CTA in a cluster
+
+// Launches, or (occupancy) returns how many CTAs or clusters run at once.
+template <typename TX, typename TG, int G, int NV, int E, int MODE, bool CL>
+int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_sms, cudaStream_t s) {
+  using Cols = NormCols<G, NV, E, MODE, CL>;
+  // three stages where they leave room for a second CTA of 256 threads
+  constexpr int S = BwdRing<TX, TG, G, NV, E, 3, MODE>::kBytes <= 110 * 1024 ? 3 : 2;
+  constexpr int kSmem = BwdRing<TX, TG, G, NV, E, S, MODE>::kBytes;
+  auto* kernel = norm_bwd_kernel<TX, TG, G, NV, E, S, MODE, CL>;
+  NormBwdParams p = params;
+  const int need = p.cols + (MODE == kPhase ? 7 : 0);
+  const int ctas = CL ? norm_cluster(need, kWideBwdCta) : 1;
+  if (CL) p.slice = norm_slice(need, ctas);
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> held{0};
+  const int per_sm = norm_occupancy(kernel, Cols::kThreads, kSmem, done, held);
   if (occupancy) {
-    static const int per_sm = norm_occupancy(kernel, kThreads);
-    return ((kThreads / G) << 16) | per_sm;
+    const int64_t most = imax64(1, static_cast<int64_t>(num_sms) * per_sm / ctas);
+    return static_cast<int>(
+        norm_blocks(imin64((p.rows + Cols::kRows - 1) / Cols::kRows, most), Cols::kRows, p.period));
   }
-  const int ctas = CL ? norm_cluster(p.cols) : 1;
-  norm_launch(kernel, parts * ctas, kThreads, ctas, p, s);
+  norm_launch(kernel, parts * ctas, Cols::kThreads, kSmem, ctas, p, s);
   return 0;
 }
 
-inline bool norm_bwd_aligned(const NormBwdParams& p) {
-  auto ok = [](const void* q, int64_t ld, int dt) {
-    return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && (ld * (dt == METIS_BF16 ? 2 : 4)) % 16 == 0;
-  };
-  return ok(p.dY, p.ldg, p.g_dtype) && (!p.X || ok(p.X, p.ldx, p.x_dtype)) && (!p.dX || ok(p.dX, p.ldd, p.dx_dtype));
-}
-
-template <typename TX, typename TG, int VEC>
-int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, cudaStream_t s) {
-  if (VEC == 8 && p.cols <= 64) return norm_bwd_go<TX, TG, VEC == 8 ? 8 : 32, 1, VEC, false>(p, parts, occ, s);
-  if (p.cols <= 256) return norm_bwd_go<TX, TG, 32, 1, VEC, false>(p, parts, occ, s);
-  if (p.cols <= 1024) return norm_bwd_go<TX, TG, 32, 4, VEC, false>(p, parts, occ, s);
-  if (p.cols <= 2048) return norm_bwd_go<TX, TG, 128, 2, VEC, false>(p, parts, occ, s);
-  if (p.cols <= 4096) return norm_bwd_go<TX, TG, 256, 2, VEC, false>(p, parts, occ, s);
-  return norm_bwd_go<TX, TG, 256, 2, VEC, true>(p, parts, occ, s);
+// E columns a unit, 32 a thread (16 where a row has 64 or fewer).
+template <typename TX, typename TG, int E, int MODE>
+int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cudaStream_t s) {
+  constexpr int NV = 32 / E, G0 = E == 8 ? 4 : 8;
+  const int cols = p.cols + (MODE == kPhase ? 7 : 0);
+  if (cols <= 64) return norm_bwd_go<TX, TG, G0, 64 / (G0 * E), E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 128) return norm_bwd_go<TX, TG, G0, 128 / (G0 * E), E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 256) return norm_bwd_go<TX, TG, 8, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 512) return norm_bwd_go<TX, TG, 16, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 1024) return norm_bwd_go<TX, TG, 32, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 2048) return norm_bwd_go<TX, TG, 64, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= 4096) return norm_bwd_go<TX, TG, 128, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  if (cols <= kWideBwdCta) return norm_bwd_go<TX, TG, 256, NV, E, MODE, false>(p, parts, occ, num_sms, s);
+  return norm_bwd_go<TX, TG, 256, NV, E, MODE, true>(p, parts, occ, num_sms, s);
 }
 
 template <typename TX>
-int norm_bwd_kind(const NormBwdParams& p, int parts, bool occ, cudaStream_t s) {
-  const bool al = norm_bwd_aligned(p);
-  if (p.g_dtype == METIS_BF16)
-    return al ? norm_bwd_cols<TX, __nv_bfloat16, 8>(p, parts, occ, s)
-              : norm_bwd_cols<TX, __nv_bfloat16, 1>(p, parts, occ, s);
-  return al ? norm_bwd_cols<TX, float, 8>(p, parts, occ, s) : norm_bwd_cols<TX, float, 1>(p, parts, occ, s);
+int norm_bwd_kind(const NormBwdParams& p, int mode, bool narrow, int parts, bool occ, int num_sms, cudaStream_t s) {
+  using H = __nv_bfloat16;
+  constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kF32 = std::is_same_v<TX, float>;
+  const bool g16 = p.g_dtype == METIS_BF16;
+  if (mode == kAny)
+    return g16 ? norm_bwd_cols<TX, H, 8, kAny>(p, parts, occ, num_sms, s)
+               : norm_bwd_cols<TX, float, 8, kAny>(p, parts, occ, num_sms, s);
+  if constexpr (kDense) {
+    if (mode == kPhase) {
+      if constexpr (!kF32)
+        if (narrow) return norm_bwd_cols<TX, H, 8, kPhase>(p, parts, occ, num_sms, s);
+      return g16 ? norm_bwd_cols<TX, H, 4, kPhase>(p, parts, occ, num_sms, s)
+                 : norm_bwd_cols<TX, float, 4, kPhase>(p, parts, occ, num_sms, s);
+    }
+  }
+  if constexpr (!kF32)
+    if (narrow) return norm_bwd_cols<TX, H, 8, kAligned>(p, parts, occ, num_sms, s);
+  return g16 ? norm_bwd_cols<TX, H, 4, kAligned>(p, parts, occ, num_sms, s)
+             : norm_bwd_cols<TX, float, 4, kAligned>(p, parts, occ, num_sms, s);
 }
 
 }  // namespace metis

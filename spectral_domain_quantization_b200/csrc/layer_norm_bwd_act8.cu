@@ -3,8 +3,8 @@
 
 namespace metis {
 
-int norm_bwd_act8(const NormBwdParams& p, int parts, bool occupancy, cudaStream_t s) {
-  return norm_bwd_kind<Act8Tag>(p, parts, occupancy, s);
+int norm_bwd_act8(const NormBwdParams& p, int mode, bool narrow, int parts, bool occupancy, int num_sms, cudaStream_t s) {
+  return norm_bwd_kind<Act8Tag>(p, mode, narrow, parts, occupancy, num_sms, s);
 }
 
 }  // namespace metis

@@ -1,0 +1,318 @@
+// Layer norm, forward: y = (x - mean) rstd w + b over the columns of each row,
+// optionally keeping x in 8 bits from the same pass.
+//
+// Bound by HBM: every element is read once and written once (and once more as
+// 1 + 1/32 bytes with the 8-bit copy).  A warp sums its part of the row, then the
+// squares of the deviations from its own mean; behind one barrier the warps' means
+// and squares are joined (Chan, Golub and LeVeque's update), relative to the first
+// warp's mean m0, so neither the variance nor the mean of a row far from zero is
+// a difference of large sums.  The row's mean stays a pair m0 + m1.  The grid is
+// no larger than what is resident at once, so a thread loads its columns' weight
+// and bias once for all its rows.
+#pragma once
+
+#include "layer_norm.cuh"
+
+namespace metis {
+
+// What the mean m of n float32 values lost, times n, from the sum r of their
+// deviations and of the deviations' squares.  Far from zero (|m| over the standard
+// deviation) the deviations are nearly exact, and r is the sum's rounding.  Near
+// zero they carry a rounding that is the same for all values of a binade, and the
+// sum itself is the better of the two.
+MDEV float sum_rest(float m, float n, float r, float squares) { return m * m * n > squares ? r : 0.f; }
+
+// The same of bf16 values with sum s: far from zero s is exact (8 bits a value, 24
+// in the sum), and what is left is the division's remainder.
+MDEV float division_rest(float m, float n, float s) { return fmaf(-m, n, s); }
+
+// What a row ends with.
+struct RowStats {
+  float m0, off, rstd, mean;    // (x - mean) rstd = (x - m0) rstd + off
+  MDEV void set(float first, float rest, float squares, float inv_n, float eps) {
+    const float v = squares < 0.f ? 0.f : squares;      // keeps a NaN
+    m0 = first;
+    rstd = inv_sqrt(fmaf(v, inv_n, eps));
+    off = -rest * rstd;
+    mean = first + rest;
+  }
+};
+
+template <typename T, int G, int NV, int E, int S, int MODE>
+struct FwdRing {
+  using C = NormCols<G, NV, E, MODE, false>;
+  using Slot = UnitSlot<T, E, MODE, C::kThreads, C::kSpan>;
+  static constexpr int kStage = NV * Slot::kBytes;
+  static constexpr int kBytes = S * kStage;
+};
+
+template <typename T, int G, int NV, int E, int S, int MODE, bool SAVE, bool CL>
+__global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdParams p, int ctas) {
+  using Cols = NormCols<G, NV, E, MODE, CL>;
+  using Ring = FwdRing<T, G, NV, E, S, MODE>;
+  using Slot = typename Ring::Slot;
+  constexpr bool kRest = sizeof(T) == 4;
+  using Ex = Exchange<G, kRest ? 3 : 2, CL>;
+  constexpr int kThreads = Cols::kThreads, kSpan = Cols::kSpan, kMost = Ex::kMost;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float parts[Ex::kFloats];
+  const Cols cs(p.cols, p.slice, ctas, p.period, p.ldx, p.offset, 8);
+  Ex ex(parts, ctas);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const T* X = static_cast<const T*>(p.X);
+  const Span span = span_of<T>(p.X, p.rows, p.cols, p.ldx);
+  const uint32_t ring0 = smem_u32(ring);
+
+  // row `fetch_row` into the stage at `into`
+  int64_t fetch_row = cs.row;
+  uint32_t into = ring0;
+  auto fetch = [&] {
+    const bool on = fetch_row < p.rows;
+    if (G < 32 || on) {
+      const T* x = X + fetch_row * p.ldx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t at = into + i * Slot::kBytes;
+        if constexpr (MODE == kAny)
+          Slot::start(at, tid, x + cs.col(i), on ? cs.left(i) : -16, cs.last, span);
+        else
+          Slot::start(at, tid, x + cs.col(i), on && cs.whole(i), on && cs.some(i), span);
+      }
+    }
+    cp_async_commit();
+    fetch_row += cs.step;
+    into = into + Ring::kStage == ring0 + Ring::kBytes ? ring0 : into + Ring::kStage;
+  };
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) fetch();
+  float w[NV * E], b[NV * E];
+  load_vector(cs, p.w, p.w_dtype, 1.f, w);
+  load_vector(cs, p.b, p.w_dtype, 0.f, b);
+  // columns of a warp of the row, as the exchange numbers them
+  auto columns_of = [&](int warp) {
+    const int r = CL ? warp / Ex::kWarps : 0;
+    const int shift = MODE == kPhase ? (CL ? static_cast<int>(cluster_rank()) * p.slice : 0) + cs.t * E - cs.c0 : 0;
+    const int b0 = (CL ? r * p.slice : 0) - shift;
+    const int e0 = CL ? min(p.cols, b0 + p.slice) : p.cols, l0 = max(b0, 0);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = b0 + (i * G + (warp % Ex::kWarps) * 32) * E;
+      n += max(min(e0, at + E * kSpan) - max(l0, at), 0);
+    }
+    return static_cast<float>(n);
+  };
+  const float n_w = columns_of(G > 32 ? (CL ? static_cast<int>(cluster_rank()) * Ex::kWarps : 0) + (tid >> 5) : 0);
+  const float inv_w = n_w > 0.f ? __fdiv_rn(1.f, n_w) : 0.f;
+  const float inv_n = __fdiv_rn(1.f, static_cast<float>(p.cols));
+  const float lane_n = G > 32 && lane < ex.warps() ? columns_of(lane) : 0.f;
+  const float inv_lane = lane_n > 0.f ? __fdiv_rn(1.f, lane_n) : 0.f;
+  float top = 0.f;
+  if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
+  uint32_t from = ring0;
+  // all threads of a row leave the loop together; with several rows in a warp,
+  // all of the warp
+  for (int64_t row = cs.row; G >= 32 ? row < p.rows : row - (lane / G) < p.rows; row += cs.step) {
+    fetch();
+    const bool active = G >= 32 || row < p.rows;
+    cp_async_wait<S - 1>();
+    float v[NV * E], part[NV];
+    Unit<T, E> kept[MODE == kAny && SAVE ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t at = from + i * Slot::kBytes;
+      Unit<T, E> u;
+      if constexpr (MODE == kAny) {
+        u = Slot::finish(at, tid, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+        if constexpr (SAVE) kept[i] = u;
+      } else {
+        u = Slot::finish(at, tid);
+        if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+      }
+      u.get(v + E * i);
+      part[i] = tree_sum<E>(v + E * i);
+    }
+    const float sum = span_sum<kSpan>(tree_sum<NV>(part));
+    const float m = divide(sum, n_w, inv_w);
+    float p2[NV], p1[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float e[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
+      if (MODE != kAligned && !cs.whole(i)) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
+      }
+      p2[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
+      if constexpr (kRest) p1[i] = tree_sum<E>(e);
+      if (MODE == kAligned && !cs.whole(i)) {
+        p2[i] = 0.f;
+        if constexpr (kRest) p1[i] = 0.f;
+      }
+    }
+    float sq = tree_sum<NV>(p2), rest = 0.f;
+    if constexpr (kRest) rest = tree_sum<NV>(p1);
+    RowStats st;
+    if constexpr (G <= 32) {
+      sq = span_sum<kSpan>(sq);
+      const float r = kRest ? sum_rest(m, n_w, span_sum<kSpan>(rest), sq) : division_rest(m, n_w, sum);
+      st.set(m, r * inv_n, fmaf(-r, r * inv_n, sq), inv_n, p.eps);
+    } else {
+      if constexpr (kRest) {
+        const float s = warp_sums2(sq, rest);
+        const float s2 = __shfl_sync(0xFFFFFFFFu, s, 0);
+        if (lane == 0) {
+          ex.put(0, sum);
+          ex.put(1, s);
+        }
+        if (lane == 16) ex.put(2, sum_rest(m, n_w, s, s2));
+      } else {
+        sq = span_sum<32>(sq);
+        if (lane == 0) {
+          ex.put(0, sum);
+          ex.put(1, sq);
+        }
+      }
+      const float* pt = ex.sync();
+      // warp k's mean relative to the first's, what it lost (mr; r times its columns)
+      const float first = divide(pt[0], columns_of(0), __fdiv_rn(1.f, columns_of(0)));
+      auto dev = [&](int k, float cw, float inv, float& r, float& mr) {
+        const float mk = divide(pt[k], cw, inv);
+        r = kRest ? pt[2 * kMost + k] : division_rest(mk, cw, pt[k]);
+        mr = r * inv;
+        return (mk - first) + mr;
+      };
+      float r, mr;
+      if constexpr (kMost <= 32) {
+        const bool in = lane_n > 0.f;
+        const float dm = in ? dev(lane % kMost, lane_n, inv_lane, r, mr) : 0.f;
+        const float shift = span_sum<kMost>(lane_n * dm) * inv_n;
+        const float e = dm - shift;
+        const float x = span_sum<kMost>(in ? fmaf(lane_n * e, e, fmaf(-r, mr, pt[kMost + lane])) : 0.f);
+        st.set(first, shift, x, inv_n, p.eps);       // right in the lanes of the row's warps
+        st.off = __shfl_sync(0xFFFFFFFFu, st.off, 0);
+        st.rstd = __shfl_sync(0xFFFFFFFFu, st.rstd, 0);
+      } else {
+        const int nw = ex.warps();
+        float s = 0.f, x = 0.f;
+        for (int k = lane; k < nw; k += 32) {
+          const float cw = columns_of(k);
+          if (cw > 0.f) s = fmaf(cw, dev(k, cw, __fdiv_rn(1.f, cw), r, mr), s);
+        }
+        const float shift = span_sum<32>(s) * inv_n;
+        for (int k = lane; k < nw; k += 32) {
+          const float cw = columns_of(k);
+          if (cw > 0.f) {
+            const float e = dev(k, cw, __fdiv_rn(1.f, cw), r, mr) - shift;
+            x += fmaf(cw * e, e, fmaf(-r, mr, pt[kMost + k]));
+          }
+        }
+        st.set(first, shift, span_sum<32>(x), inv_n, p.eps);
+      }
+    }
+    if (active && cs.t == 0 && (!CL || cluster_rank() == 0)) {
+      if (p.mean) p.mean[row] = st.mean;
+      if (p.rstd) p.rstd[row] = st.rstd;
+    }
+    void* y = static_cast<char*>(p.Y) + row * p.ldy * (p.y_dtype == METIS_BF16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int k = E * i + j;
+        o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
+      }
+      store_row_unit_any(cs, y, p.y_dtype, o, i, active);
+      if constexpr (SAVE) {
+        Unit<T, E> u;
+        if constexpr (MODE == kAny)
+          u = kept[i];
+        else
+          u = Slot::finish(from + i * Slot::kBytes, tid);
+        float x[E];
+        u.get(x);
+        uint32_t codes[E / 4];
+        const uint32_t sc = p.save.fmt == METIS_MXINT8 ? act8_block<METIS_MXINT8, E>(x, codes, top)
+                                                       : act8_block<METIS_MXFP8, E>(x, codes, top);
+        const int c = cs.col(i);
+        const int pad = CL ? min(static_cast<int>(p.save.ldc), cs.lo + p.slice) : static_cast<int>(p.save.ldc);
+        if (active && c < pad) {
+          uint8_t* dst = p.save.codes + row * p.save.ldc + c;
+          if constexpr (E == 8)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+          else
+            *reinterpret_cast<uint32_t*>(dst) = codes[0];
+          if (cs.t % (32 / E) == 0) p.save.scales[row * p.save.blocks + (c >> 5)] = static_cast<uint8_t>(sc);
+        }
+      }
+    }
+    from = from + Ring::kStage == ring0 + Ring::kBytes ? ring0 : from + Ring::kStage;
+  }
+  cp_async_wait<0>();
+  if constexpr (SAVE) {
+    __shared__ float wm[kThreads / 32];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    if (lane == 0) wm[tid >> 5] = top;
+    __syncthreads();
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, wm[i]);
+    act8_write_amax(p.save.amax,
+                    p.save.fmt == METIS_MXINT8 ? act8_held<METIS_MXINT8>(top) : act8_held<METIS_MXFP8>(top));
+  }
+}
+
+constexpr int kWideCta = 512 * 32;      // columns of a CTA in a cluster
+
+template <typename T, int G, int NV, int E, int MODE, bool SAVE, bool CL>
+void norm_fwd_go(const NormFwdParams& params, int num_sms, cudaStream_t s) {
+  using Cols = NormCols<G, NV, E, MODE, CL>;
+  constexpr int S = 3;
+  constexpr int kSmem = FwdRing<T, G, NV, E, S, MODE>::kBytes;
+  auto* kernel = norm_fwd_kernel<T, G, NV, E, S, MODE, SAVE, CL>;
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> held{0};
+  const int per_sm = norm_occupancy(kernel, Cols::kThreads, kSmem, done, held);
+  NormFwdParams p = params;
+  const int need = p.cols + (MODE == kPhase ? 7 : 0);
+  const int ctas = CL ? norm_cluster(need, kWideCta) : 1;
+  if (CL) p.slice = norm_slice(need, ctas);
+  const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX) / ctas;
+  const int64_t blocks = imin64((p.rows + Cols::kRows - 1) / Cols::kRows, imax64(1, most));
+  norm_launch(kernel, static_cast<int>(norm_blocks(blocks, Cols::kRows, p.period)) * ctas, Cols::kThreads, kSmem, ctas,
+              p, s);
+}
+
+// E columns a unit, 32 a thread (16 where a row has 64 or fewer).
+template <typename T, int E, int MODE, bool SAVE>
+void norm_fwd_cols(const NormFwdParams& p, int num_sms, cudaStream_t s) {
+  constexpr int NV = 32 / E, G0 = E == 8 ? 4 : 8;      // a block of 32 columns lies in 32 / E lanes
+  const int cols = p.cols + (MODE == kPhase ? 7 : 0);
+  if (cols <= 64)
+    norm_fwd_go<T, G0, 64 / (G0 * E), E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 128)
+    norm_fwd_go<T, G0, 128 / (G0 * E), E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 256)
+    norm_fwd_go<T, 8, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 512)
+    norm_fwd_go<T, 16, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 1024)
+    norm_fwd_go<T, 32, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 2048)
+    norm_fwd_go<T, 64, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 4096)
+    norm_fwd_go<T, 128, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= 8192)
+    norm_fwd_go<T, 256, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else if (cols <= kWideCta)
+    norm_fwd_go<T, 512, NV, E, MODE, SAVE, false>(p, num_sms, s);
+  else
+    norm_fwd_go<T, 512, NV, E, MODE, SAVE, true>(p, num_sms, s);
+}
+
+}  // namespace metis

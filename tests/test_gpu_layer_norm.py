@@ -91,8 +91,9 @@ def check_bwd(got, dY, x64, mean, rstd, w):
 SHAPES = [(1, 1, 0, 0), (3, 1, 0, 0), (1, 4096, 0, 0), (2, 7, 0, 0), (37, 32, 0, 0), (5, 64, 0, 0), (9, 65, 0, 0),
           (300, 200, 0, 0), (11, 256, 0, 0), (70, 257, 0, 0), (33, 1000, 24, 0), (6, 1003, 0, 0), (5, 1024, 1, 1),
           (4, 1027, 0, 0), (3, 2048, 0, 0), (3, 2056, 8, 8), (5, 4095, 0, 0), (700, 4096, 0, 0), (3, 4097, 0, 0),
-          (40, 5000, 0, 0), (9, 8200, 0, 0), (3, 14336, 0, 0), (2, 16391, 0, 0), (2, 32768, 0, 0), (2, 32771, 0, 0),
-          (1, 40000, 0, 0), (2000, 72, 0, 0), (5000, 33, 0, 0)]
+          (40, 5000, 0, 0), (9, 8200, 0, 0), (3, 14336, 0, 0), (2, 16391, 0, 0), (2, 32768, 0, 0), (2, 32765, 0, 0), (9, 16383, 0, 0), (20, 8190, 0, 3), (2, 32771, 0, 0),
+          (1, 40000, 0, 0), (2000, 72, 0, 0), (5000, 33, 0, 0), (700, 57, 0, 0), (90, 121, 0, 5), (301, 255, 0, 1), (40, 510, 2, 0),
+          (77, 2046, 0, 0), (19, 128, 4, 4)]
 
 
 @pytest.mark.parametrize("dtype,wdtype,out", [("bf16", "f32", "bf16"), ("f32", "f32", "f32"), ("bf16", "bf16", "f32"),
@@ -156,11 +157,12 @@ def test_many_rows():
 
 @pytest.mark.parametrize("cols", [64, 1000, 4096, 6001, 33000])
 @pytest.mark.parametrize("shift", [1000.0, -30000.0])
-def test_large_offset(cols, shift):
-    # the variance of a row far from zero: no cancellation
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_offset(cols, shift, dtype):
+    # a row far from zero: no cancellation in the variance, no bits lost in the mean
     x, _, w, b = data(4, cols, seed=4, shift=shift)
-    X = mat(x, "f32")
-    check_fwd(api.layer_norm_fwd(X, w.cuda(), b.cuda()), X, w, b)
+    X = mat(x, dtype)
+    check_fwd(api.layer_norm_fwd(X, w.cuda(), b.cuda(), out_dtype=torch.float32), X, w, b)
 
 
 @pytest.mark.parametrize("cols", [64, 255, 1000, 4096, 6000, 33000])
