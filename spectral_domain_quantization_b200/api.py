@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "libmetis_b200.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "metis.h")
 
 OK = 0
+ERR_WORKSPACE = 5
 BF16, F32 = 0, 1
 MXFP4, NVFP4 = 0, 1
 SKETCH_GAUSSIAN, SKETCH_SPARSE_SIGN = 0, 1
@@ -147,8 +148,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(index):
+    """The current stream of device `index` (a cudaStream_t as an integer)."""
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return _stream_of(torch.cuda.current_device())
 
 
 def _dtype_code(t):
@@ -162,13 +173,25 @@ def _dtype_code(t):
 class _Workspace:
     """Grow-only workspace per device and stream (allocated by torch, the
     caller side), so that calls enqueued on different streams never share
-    scratch memory."""
+    scratch memory.  A call that is captured into a graph gets memory of its
+    own, from the graph's pool: graphs captured on one stream may be replayed
+    at the same time, and live longer than a buffer that grows."""
 
     def __init__(self):
         self.buf = {}
 
+    def held(self, device):
+        """The stream's buffer as it is; None if there is none, or in a capture."""
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        index = device.index if device.index is not None else torch.cuda.current_device()
+        return self.buf.get((index, _stream_of(index)))
+
     def get(self, nbytes, device):
-        key = (torch.device(device).index, torch.cuda.current_stream(device).cuda_stream)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+        index = device.index if device.index is not None else torch.cuda.current_device()
+        key = (index, _stream_of(index))
         cur = self.buf.get(key)
         if cur is None or cur.numel() < nbytes:
             cur = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -180,8 +203,19 @@ _ws = _Workspace()
 
 
 def _call_with_workspace(fn, args_before_ws, args_after_ws, device, what, workspace=None):
-    """Query the workspace size, provide it (the caller's uint8 tensor when
-    given, else the shared per-stream one), then run the call."""
+    """Provide a workspace (the caller's uint8 tensor when given, else the
+    shared per-stream one, grown to the size the call asks for), then run the
+    call."""
+    if workspace is None:
+        ws = _ws.held(device)
+        if ws is not None:
+            # large enough in most calls: the library refuses it otherwise,
+            # before anything is launched
+            size = ctypes.c_size_t(ws.numel())
+            status = fn(*args_before_ws, ws.data_ptr(), ctypes.byref(size), *args_after_ws)
+            if status != ERR_WORKSPACE:
+                _check(status, what)
+                return
     size = ctypes.c_size_t(0)
     _check(fn(*args_before_ws, None, ctypes.byref(size), *args_after_ws), what + " (workspace query)")
     if workspace is not None:
@@ -198,10 +232,25 @@ def _call_with_workspace(fn, args_before_ws, args_after_ws, device, what, worksp
 # FP4 tensors
 # --------------------------------------------------------------------------
 
+_ones = {}
+
+
+def _one(device):
+    """A float32 1 on `device` that nothing writes (MXFP4 has no tensor scale)."""
+    t = _ones.get(device)
+    if t is None:
+        t = torch.ones(1, dtype=torch.float32, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(device).synchronize()     # other streams may read it
+            _ones[device] = t
+    return t
+
+
 class QTensor:
     """An FP4 matrix (outer x inner, blocks along inner) held in torch buffers."""
 
-    def __init__(self, fmt, outer, inner, device="cuda", linear=False, inner_sum=False):
+    def __init__(self, fmt, outer, inner, device="cuda", linear=False, inner_sum=False, written=False):
+        # written: the call this is made for writes tensor_scale (NVFP4)
         L = lib()
         self.fmt = FMT[fmt]
         self.outer, self.inner = int(outer), int(inner)
@@ -212,7 +261,12 @@ class QTensor:
                                   dtype=torch.uint8, device=device)
         self.scales_linear = (torch.empty(self.outer * (self.inner // self.block), dtype=torch.uint8,
                                           device=device) if linear else None)
-        self.tensor_scale = torch.ones(1, dtype=torch.float32, device=device)
+        if not written:
+            self.tensor_scale = torch.ones(1, dtype=torch.float32, device=device)
+        elif self.fmt == NVFP4:
+            self.tensor_scale = torch.empty(1, dtype=torch.float32, device=device)
+        else:
+            self.tensor_scale = _one(self.codes.device)
         self.inner_sum = torch.empty(self.outer, dtype=torch.float32, device=device) if inner_sum else None
 
     def struct(self):
@@ -234,7 +288,7 @@ def quantize_fp4(X, fmt, axis=1, sub_col=None, linear=False, inner_sum=False, ou
     rows, cols = X.shape
     outer, inner = (rows, cols) if axis == 1 else (cols, rows)
     if out is None:
-        out = QTensor(fmt, outer, inner, X.device, linear=linear, inner_sum=inner_sum)
+        out = QTensor(fmt, outer, inner, X.device, linear=linear, inner_sum=inner_sum, written=True)
     s = out.struct()
     L = lib()
     _call_with_workspace(
@@ -304,7 +358,7 @@ def linear_fwd(X, W, M, N, K, out_dtype=torch.float32, Y=None, dev_status=None):
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=dev)
     if dev_status is None:
-        dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        dev_status = torch.empty(1, dtype=torch.int32, device=dev)      # nobody reads it
     xs, ws_ = X.struct(), W.struct()
     _call_with_workspace(
         lib().metis_linear_fwd,
@@ -322,7 +376,7 @@ def linear_bwd(dY_n, Wt, Xt, dY_m, M, N, K, out_dtype=torch.float32, dX=None, dW
     if want_dw and dW is None:
         dW = torch.empty((K, N), dtype=out_dtype, device=dev)
     if dev_status is None:
-        dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        dev_status = torch.empty(1, dtype=torch.int32, device=dev)      # nobody reads it
     a = ctypes.byref(dY_n.struct()) if want_dx else None
     b = ctypes.byref(Wt.struct()) if want_dx else None
     c = ctypes.byref(Xt.struct()) if want_dw else None
@@ -564,12 +618,13 @@ def _on_device(t, name, device=None):
 
 
 def _vector(t, name, n, device, dtypes):
-    """Check a contiguous CUDA vector of n elements."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    """Check a contiguous vector of n elements on `device`."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    _on_device(t, name, device)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _out_matrix(t, name, shape, device):
@@ -579,24 +634,15 @@ def _out_matrix(t, name, shape, device):
     return ld
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(device):
-    """The current stream of `device` (a cudaStream_t as an integer)."""
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _run_on(device, fn, what, *args):
     """fn(*args) with `device` current (the library launches on the current
     device); args end with that device's current stream."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, _stream_of(device)), what)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, _stream_of(index)), what)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream_of(device)), what)
+            _check(fn(*args, _stream_of(index)), what)
 
 
 class Act8:
@@ -617,25 +663,37 @@ class Act8:
             raise ValueError("an 8-bit matrix has at least 0 rows and 1 column")
         self.blocks = nb = (self.cols + 31) // 32
         if codes is None and scales is None and amax is None:
-            codes = torch.empty((self.rows, 32 * nb), dtype=torch.uint8, device=device)
-            scales = torch.empty((self.rows, nb), dtype=torch.uint8, device=device)
-            amax = torch.empty(ACT8_AMAX, dtype=torch.float32, device=device)
+            # one buffer; the tensors of its parts are made when they are asked for
+            n = self.rows * nb
+            self._buf = torch.empty(4 * ACT8_AMAX + 33 * n, dtype=torch.uint8, device=device)
+            self.device = self._buf.device
+            at = self._buf.data_ptr()
+            at = (at, at + 4 * ACT8_AMAX, at + 4 * ACT8_AMAX + 32 * n)
         else:
             for name, t, shape, dt in (("codes", codes, (self.rows, 32 * nb), torch.uint8),
                                        ("scales", scales, (self.rows, nb), torch.uint8),
                                        ("amax", amax, (ACT8_AMAX,), torch.float32)):
-                if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != dt \
-                        or not t.is_contiguous():
+                if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dt or not t.is_contiguous():
                     raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
                 _on_device(t, name, codes.device)
-        self.codes, self.scales, self.amax = codes, scales, amax
-        self.device = codes.device
-        self._s = Act8Struct(ACT8_FMT[fmt], self.rows, self.cols, codes.data_ptr(), scales.data_ptr(),
-                             amax.data_ptr())
+            self.codes, self.scales, self.amax = codes, scales, amax
+            self.device = codes.device
+            at = (amax.data_ptr(), codes.data_ptr(), scales.data_ptr())
+        self._s = Act8Struct(ACT8_FMT[fmt], self.rows, self.cols, at[1], at[2], at[0])
+
+    def __getattr__(self, name):
+        # reached for what is not set yet
+        if name in ("codes", "scales", "amax") and "_buf" in self.__dict__:
+            n, a = self.rows * self.blocks, 4 * ACT8_AMAX
+            self.amax = self._buf[:a].view(torch.float32)
+            self.codes = self._buf[a:a + 32 * n].view(self.rows, 32 * self.blocks)
+            self.scales = self._buf[a + 32 * n:].view(self.rows, self.blocks)
+            return self.__dict__[name]
+        raise AttributeError(name)
 
     @property
     def nbytes(self):
-        return self.codes.numel() + self.scales.numel() + 4 * ACT8_AMAX
+        return 33 * self.rows * self.blocks + 4 * ACT8_AMAX
 
 
 def _act8_out(out, fmt, rows, cols, device):
@@ -643,7 +701,8 @@ def _act8_out(out, fmt, rows, cols, device):
         return Act8(fmt, rows, cols, device)
     if not isinstance(out, Act8) or (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
         raise ValueError(f"out must be an Act8 of {rows} x {cols} in {fmt}")
-    _on_device(out.codes, "out", device)
+    if out.device != device:
+        raise ValueError(f"out is on {out.device}, not on {device}")
     return out
 
 
@@ -665,7 +724,7 @@ def restore_act8(a, dtype=torch.bfloat16, out=None):
     if out is None:
         if dtype not in _DTYPE_CODE:
             raise TypeError("only bfloat16 and float32 outputs are supported")
-        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.device)
+        out = torch.empty(a.rows, a.cols, dtype=dtype, device=a.device)
         ld = a.cols
     else:
         ld = _out_matrix(out, "out", (a.rows, a.cols), a.device)
@@ -686,7 +745,7 @@ def quantize_fp4_act8(a, fmt, axis=1, linear=False, out=None):
     if inner % 32 or outer == 0 or inner == 0:
         raise ValueError(f"the blocked dimension must be a multiple of 32 (it is {inner}) and no dimension 0")
     if out is None:
-        out = QTensor(fmt, outer, inner, a.device, linear=linear)
+        out = QTensor(fmt, outer, inner, a.device, linear=linear, written=True)
     elif (out.fmt, out.outer, out.inner) != (FMT[fmt], outer, inner) or out.codes.device != a.device:
         raise ValueError(f"out must be a QTensor of {outer} x {inner} on {a.device}")
     _run_on(a.device, lib().metis_act8_quantize_fp4, "metis_act8_quantize_fp4",
@@ -706,15 +765,17 @@ class LayerNorm:
 
 def _affine(weight, bias, cols, device):
     """Pointers of weight and bias (either may be None) and their dtype code."""
-    dt = None
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _vector(t, name, cols, device, _DTYPE_CODE)
-            if dt is not None and t.dtype != dt:
-                raise TypeError("weight and bias must have one dtype")
-            dt = t.dtype
-    return (None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
-            BF16 if dt is None else _DTYPE_CODE[dt])
+    w = b = None
+    code = BF16
+    if weight is not None:
+        _vector(weight, "weight", cols, device, _DTYPE_CODE)
+        code, w = _DTYPE_CODE[weight.dtype], weight.data_ptr()
+    if bias is not None:
+        _vector(bias, "bias", cols, device, _DTYPE_CODE)
+        if weight is not None and weight.dtype != bias.dtype:
+            raise TypeError("weight and bias must have one dtype")
+        code, b = _DTYPE_CODE[bias.dtype], bias.data_ptr()
+    return w, b, code
 
 
 def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=None, stats=True, out=None):
@@ -732,7 +793,7 @@ def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=Non
     if not eps >= 0:
         raise ValueError("eps must be 0 or more")
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype or X.dtype, device=dev)
+        out = torch.empty(rows, cols, dtype=out_dtype or X.dtype, device=dev)
         if out.dtype not in _DTYPE_CODE:
             raise TypeError("only bfloat16 and float32 outputs are supported")
         ldy = cols
@@ -766,7 +827,8 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
     if isinstance(X, Act8):
         if (X.rows, X.cols) != (rows, cols):
             raise ValueError(f"X is {X.rows} x {X.cols}, dY {rows} x {cols}")
-        _on_device(X.codes, "X", dev)
+        if X.device != dev:
+            raise ValueError(f"X is on {X.device}, not on {dev}")
         sp = ctypes.byref(X._s)
     else:
         ldx = _matrix(X, "X", dev)
@@ -779,7 +841,7 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
     ldd, dp, ddt = cols, None, BF16
     if want_dx:
         if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype or dY.dtype, device=dev)
+            out = torch.empty(rows, cols, dtype=out_dtype or dY.dtype, device=dev)
             if out.dtype not in _DTYPE_CODE:
                 raise TypeError("only bfloat16 and float32 outputs are supported")
         else:
@@ -789,16 +851,15 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
         out = None
     dw = torch.empty(cols, dtype=torch.float32, device=dev) if want_dw else None
     db = torch.empty(cols, dtype=torch.float32, device=dev) if want_db else None
-    size = ctypes.c_size_t(0)
     args = (dY.data_ptr(), _DTYPE_CODE[dY.dtype], rows, cols, ldg, xp, xdt, ldx, sp,
             mean.data_ptr() if rows else None, rstd.data_ptr() if rows else None, w, wdt, dp, ddt, ldd,
             None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
     fn = lib().metis_layer_norm_bwd
-    _run_on(dev, fn, "metis_layer_norm_bwd (workspace query)", *args, None, ctypes.byref(size))
-    # a workspace of this call alone: it stays with the stream's allocator, or
-    # with the graph that captures the call
-    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
-    _run_on(dev, fn, "metis_layer_norm_bwd", *args, ws.data_ptr(), ctypes.byref(size))
+    if torch.cuda.current_device() == dev.index:
+        _call_with_workspace(fn, args, (_stream_of(dev.index),), dev, "metis_layer_norm_bwd")
+    else:
+        with torch.cuda.device(dev):
+            _call_with_workspace(fn, args, (_stream_of(dev.index),), dev, "metis_layer_norm_bwd")
     return out, dw, db
 
 

@@ -1,14 +1,14 @@
 // What the layer norm's forward and backward kernels share: how rows are spread
 // over threads, and the sums over a row.
 //
-// A row is held in registers by G threads: part of a warp, a warp, a CTA, or a
-// cluster of CTAs that take a slice of the columns each (sums meet in
-// distributed shared memory).  Each thread has NV units of E consecutive columns
-// (rows.cuh), the same columns in every row: 32 columns a thread, so what a row
-// costs besides its elements (reductions, roots, addresses) is spread over many.
-// E is 8 where every matrix is bf16 (16-byte words) and 4 where one is float32, so
-// that a warp's words are contiguous.  The rows to come wait in a ring in shared
-// memory.
+// A row is held in registers: by SPAN lanes of a warp (up to 1024 columns), by the
+// W warps of a CTA, 1024 columns each, or by a cluster of CTAs that take a slice of
+// the columns each (sums meet in distributed shared memory).  Each thread has NV
+// units of E consecutive columns (rows.cuh), the same columns in every row: 32
+// columns a thread, so what a row costs besides its elements (reductions, roots,
+// addresses) is spread over many.  E is 8 where every matrix is bf16 (16-byte words)
+// and 4 where one is float32, so that a warp's words are contiguous.  The rows to
+// come wait in a ring in shared memory, each warp's part in a ring of its own.
 #pragma once
 
 #include <atomic>
@@ -20,41 +20,46 @@
 
 namespace metis {
 
-template <int G>
-constexpr int norm_threads() {
-  return G >= 64 ? G : 128;
-}
+// How a kernel spreads rows: kLanes, the SPAN lanes of a warp hold a row, and a
+// CTA of 128 threads takes 128 / SPAN of them; kCta, a CTA holds a row; kCluster.
+enum NormShape { kLanes = 0, kCta = 1, kCluster = 2 };
+
+constexpr int kLaneThreads = 128;
+constexpr int kWarpCols = 1024;        // columns of a warp of kCta and kCluster
 
 // The columns and rows of one thread.
-template <int G, int NV, int E, int MODE, bool CL>
+template <int SPAN, int NV, int E, int MODE, int SHAPE>
 struct NormCols {
-  static constexpr int kSpan = G < 32 ? G : 32;   // lanes of one row in a warp
-  static constexpr int kThreads = norm_threads<G>();
-  static constexpr int kRows = kThreads / G;      // rows a CTA has at once
-  int lo, hi;       // this CTA's columns
-  int c0;           // this thread's first column (kPhase: may be outside)
-  int t;            // thread within the row's threads of this CTA
-  bool first, last; // lane of the row's lanes in the warp
+  static constexpr int kSpan = SPAN;
+  static constexpr bool kMulti = SHAPE != kLanes;
+  static constexpr bool kClustered = SHAPE == kCluster;
+  static constexpr int kRows = kMulti ? 1 : kLaneThreads / SPAN;   // rows a CTA has at once
+  static constexpr int kStride = SPAN * E;                         // columns between a thread's units
+  static constexpr int kOwn = NV * E;
+  static_assert(!kMulti || SPAN * kOwn == kWarpCols);
+  int lo, hi;         // this CTA's columns
+  int c0;             // this thread's first column (kPhase: may be outside)
+  int shift;          // kPhase: columns that c0 is moved by
+  int t;              // lane of the row's lanes in the warp
+  bool first, last;   // it is the first, the last of them
   int64_t row, step;  // first row, and from one to the next
 
-  // `period`, `ld`, `offset` (kPhase): row r's first element is (offset + r ld) mod
-  // `width` elements behind a period's begin; that of rows `period` apart is equal
-  MDEV NormCols(int cols, int slice, int ctas, int period, int64_t ld, int offset, int width) {
-    t = static_cast<int>(threadIdx.x) % G;
-    first = t % kSpan == 0;
-    last = t % kSpan == kSpan - 1;
-    const int64_t blocks = CL ? gridDim.x / ctas : gridDim.x;
-    const int64_t group = static_cast<int64_t>(CL ? blockIdx.x / ctas : blockIdx.x) * kRows + threadIdx.x / G;
-    int shift = 0;
-    row = group;
+  // kPhase: row r's first element is (offset + r ld) mod `width` elements behind a
+  // period's begin; that of rows `period` apart is equal
+  MDEV NormCols(int cols, int slice, int ctas, int64_t ld, int offset, int width) {
+    t = static_cast<int>(threadIdx.x) % SPAN;
+    first = t == 0;
+    last = t == SPAN - 1;
+    const int64_t blocks = kClustered ? gridDim.x / ctas : gridDim.x;
+    row = static_cast<int64_t>(kClustered ? blockIdx.x / ctas : blockIdx.x) * kRows + (kMulti ? 0 : threadIdx.x / SPAN);
     step = blocks * kRows;                // a multiple of the period
-    if constexpr (MODE == kPhase) shift = static_cast<int>((offset + row * ld) & (width - 1));
-    const int begin = CL ? static_cast<int>(cluster_rank()) * slice - shift : -shift;
-    c0 = begin + t * E;
+    shift = MODE == kPhase ? static_cast<int>((offset + row * ld) & (width - 1)) : 0;
+    const int begin = (kClustered ? static_cast<int>(cluster_rank()) * slice : 0) - shift;
+    c0 = begin + t * E + (kMulti ? static_cast<int>(threadIdx.x >> 5) * kWarpCols : 0);
     lo = max(begin, 0);
-    hi = CL ? min(cols, begin + slice) : cols;
+    hi = kClustered ? min(cols, begin + slice) : cols;
   }
-  MDEV int col(int i) const { return c0 + i * (G * E); }
+  MDEV int col(int i) const { return c0 + i * kStride; }
   MDEV int left(int i) const { return hi - col(i); }      // columns from unit i's first on
   MDEV bool some(int i) const { return MODE == kPhase ? col(i) < hi && col(i) + E > lo : col(i) < hi; }
   MDEV bool whole(int i) const {
@@ -64,8 +69,8 @@ struct NormCols {
 };
 
 // Per-column vector (weight or bias) into registers; `none` where it is absent.
-template <int G, int NV, int E, int MODE, bool CL>
-MDEV void load_vector(const NormCols<G, NV, E, MODE, CL>& cs, const void* p, int dtype, float none, float* out) {
+template <int SPAN, int NV, int E, int MODE, int SHAPE>
+MDEV void load_vector(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, const void* p, int dtype, float none, float* out) {
   if (!p) {
 #pragma unroll
     for (int k = 0; k < NV * E; ++k) out[k] = none;
@@ -106,8 +111,8 @@ MDEV void load_vector(const NormCols<G, NV, E, MODE, CL>& cs, const void* p, int
 }
 
 // Unit i of an output row of type TY at `p` (its first column's place).
-template <typename TY, int G, int NV, int E, int MODE, bool CL>
-MDEV void store_row_unit(const NormCols<G, NV, E, MODE, CL>& cs, TY* p, const float* v, int i, bool active) {
+template <typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
+MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, const float* v, int i, bool active) {
   if constexpr (MODE == kAny) {
     Unit<TY> u;
     u.put(v);
@@ -126,8 +131,8 @@ MDEV void store_row_unit(const NormCols<G, NV, E, MODE, CL>& cs, TY* p, const fl
 }
 
 // y: the row's place of column 0, in bytes.
-template <int G, int NV, int E, int MODE, bool CL>
-MDEV void store_row_unit_any(const NormCols<G, NV, E, MODE, CL>& cs, void* y, int dtype, const float* v, int i,
+template <int SPAN, int NV, int E, int MODE, int SHAPE>
+MDEV void store_row_unit_any(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, void* y, int dtype, const float* v, int i,
                              bool active) {
   if (dtype == METIS_BF16)
     store_row_unit(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
@@ -189,46 +194,44 @@ MDEV float cta_sum(float x, float* buf) {
 }
 
 // V floats of every warp of a row's CTA or cluster, exchanged through shared
-// memory: put() (lanes that hold one), then sync(), then at().  Two buffers in
-// turn: a buffer is written again only after every thread has passed the barrier
-// that follows its last reading.
-template <int G, int V, bool CL>
+// memory: put() (lanes that hold one), then sync().  Two buffers in turn: a buffer
+// is written again only after every thread has passed the barrier that follows its
+// last reading.
+template <int V, int SHAPE>
 struct Exchange {
-  static constexpr int kWarps = G / 32 > 0 ? G / 32 : 1;
-  static constexpr int kMost = (CL ? 4 : 1) * kWarps;    // warps of a row (a power of two)
-  static constexpr int kFloats = 2 * V * kMost;
+  static constexpr int kMost = SHAPE == kCluster ? 64 : 16;    // warps of a row
+  static constexpr int kFloats = SHAPE == kLanes ? 1 : 2 * V * kMost;
   float* buf;
+  int warps;        // of a row
   int ctas;
   int phase = 0;
-  MDEV Exchange(float* b, int n) : buf(b), ctas(n) {}
-  MDEV int warps() const { return CL ? ctas * kWarps : kWarps; }
+  MDEV Exchange(float* b, int n) : buf(b), warps(SHAPE == kCluster ? n * (blockDim.x >> 5) : blockDim.x >> 5), ctas(n) {}
+  MDEV int mine() const {
+    return static_cast<int>(threadIdx.x >> 5) +
+           (SHAPE == kCluster ? static_cast<int>(cluster_rank()) * static_cast<int>(blockDim.x >> 5) : 0);
+  }
   MDEV void put(int value, float x) {
-    const int warp = threadIdx.x >> 5;
-    float* b = buf + phase * (V * kMost) + value * kMost;
-    if constexpr (CL) {
+    float* b = buf + phase * (V * kMost) + value * kMost + mine();
+    if constexpr (SHAPE == kCluster) {
       // into every CTA of the cluster
-      const uint32_t at = smem_u32(b + static_cast<int>(cluster_rank()) * kWarps + warp);
+      const uint32_t at = smem_u32(b);
       for (int r = 0; r < ctas; ++r)
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(at, static_cast<uint32_t>(r))), "f"(x)
                      : "memory");
     } else {
-      b[warp] = x;
+      *b = x;
     }
   }
   MDEV const float* sync() {
     const float* b = buf + phase * (V * kMost);
     phase ^= 1;
-    if constexpr (CL)
+    if constexpr (SHAPE == kCluster)
       cluster_sync_all();
     else
       __syncthreads();
     return b;
   }
 };
-
-// Clusters: two CTAs of up to `per` columns each, or four.
-inline int norm_cluster(int cols, int per) { return cols <= 2 * per ? 2 : 4; }
-inline int norm_slice(int cols, int ctas) { return ((cols + ctas - 1) / ctas + 31) / 32 * 32; }
 
 // CTAs (or clusters) of `rows` groups each, up to `blocks` but so many that the
 // groups are a multiple of the rows' period.
@@ -255,23 +258,42 @@ void norm_launch(void (*kernel)(P, int), int grid, int threads, int smem, int ct
   cudaLaunchKernelEx(&cfg, kernel, p, ctas);
 }
 
-// CTAs of `kernel` that an SM holds.  The limit of dynamic shared memory is an
-// attribute of the kernel on each device: `done` has a bit for every device it
-// was raised on.
-template <typename K>
-int norm_occupancy(K kernel, int threads, int smem, std::atomic<uint64_t>& done, std::atomic<int>& per_sm) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-    per_sm.store(n, std::memory_order_relaxed);
-    done.fetch_or(bit, std::memory_order_release);
+// What is known of a kernel: the CTAs of W warps that an SM holds, and on which
+// devices its limit of dynamic shared memory has been raised (an attribute of the
+// kernel on each device).
+struct NormHeld {
+  std::atomic<uint64_t> devices{0};
+  std::atomic<int> per_sm[17]{};
+  template <typename K>
+  int get(K kernel, int warps, int smem, int most_smem) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(devices.load(std::memory_order_acquire) & bit)) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+      devices.fetch_or(bit, std::memory_order_release);
+    }
+    int n = per_sm[warps].load(std::memory_order_relaxed);
+    if (n == 0) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * warps, smem) != cudaSuccess || n < 1) n = 1;
+      per_sm[warps].store(n, std::memory_order_relaxed);
+    }
+    return n;
   }
-  return per_sm.load(std::memory_order_relaxed);
-}
+};
+
+// The launch of one kernel for `cols` columns, `most` warps to a CTA.
+struct NormPlan {
+  int ctas = 1, warps = kLaneThreads / 32, slice = 0;
+  NormPlan(int shape, int cols, int most) {
+    if (shape == kLanes) return;
+    if (shape == kCluster) {
+      ctas = cols <= 2 * most * kWarpCols ? 2 : 4;
+      slice = ((cols + ctas - 1) / ctas + 31) / 32 * 32;
+    }
+    warps = ((shape == kCluster ? slice : cols) + kWarpCols - 1) / kWarpCols;
+  }
+};
 
 // A matrix of a call, for the choice of the kernels' row mode.
 struct RowsOf {

@@ -15,15 +15,14 @@ namespace metis {
 
 struct Act8Tag {};
 
-// A unit of x in the ring: a dense one, or E codes of the 8-bit copy.
-template <typename TX, int E, int MODE, int kThreads, int kSpan>
-struct XSlot {
-  using Slot = UnitSlot<TX, E, MODE, kThreads, kSpan>;
-  static constexpr int kBytes = Slot::kBytes;
+// Bytes of a unit of x in the ring, of a warp: dense, or E codes of the 8-bit copy.
+template <typename TX, int E, int MODE, int SPAN>
+struct XBytes {
+  static constexpr int value = UnitSlot<TX, E, MODE, 32, SPAN>::kBytes;
 };
-template <int E, int MODE, int kThreads, int kSpan>
-struct XSlot<Act8Tag, E, MODE, kThreads, kSpan> {
-  static constexpr int kBytes = E * kThreads;
+template <int E, int MODE, int SPAN>
+struct XBytes<Act8Tag, E, MODE, SPAN> {
+  static constexpr int value = E * 32;
 };
 
 // x of one unit.
@@ -61,38 +60,36 @@ struct DenseType<Act8Tag> {
   using type = float;   // not used
 };
 
-template <typename TX, typename TG, int G, int NV, int E, int S, int MODE>
-struct BwdRing {
-  using C = NormCols<G, NV, E, MODE, false>;
-  using GS = UnitSlot<TG, E, MODE, C::kThreads, C::kSpan>;
-  using XS = XSlot<TX, E, MODE, C::kThreads, C::kSpan>;
-  static constexpr int kOne = GS::kBytes + XS::kBytes;
-  static constexpr int kStage = NV * kOne;
-  static constexpr int kGather = C::kRows > 1 ? C::kThreads * NV * E * 4 : 0;
-  static constexpr int kBytes = S * kStage > kGather ? S * kStage : kGather;
+template <typename TX, typename TG, int SPAN, int NV, int E, int MODE>
+struct BwdStage {
+  static constexpr int kG = UnitSlot<TG, E, MODE, 32, SPAN>::kBytes;
+  static constexpr int kOne = kG + XBytes<TX, E, MODE, SPAN>::value;
+  static constexpr int kBytes = NV * kOne;      // of a warp
 };
 
-template <typename TX, typename TG, int G, int NV, int E, int S, int MODE, bool CL>
-__global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdParams p, int ctas) {
-  using Cols = NormCols<G, NV, E, MODE, CL>;
-  using Ring = BwdRing<TX, TG, G, NV, E, S, MODE>;
-  using GS = typename Ring::GS;
+constexpr int kBwdWarps = 8;       // of a CTA
+
+template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, int SHAPE>
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd_kernel(NormBwdParams p, int ctas) {
+  using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
+  using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
+  using GS = UnitSlot<TG, E, MODE, 32, SPAN>;
   using DX = typename DenseType<TX>::type;
-  using XS = UnitSlot<DX, E, MODE, Cols::kThreads, Cols::kSpan>;   // dense x
-  using Ex = Exchange<G, 2, CL>;
-  constexpr bool kDense = !std::is_same_v<TX, Act8Tag>;
-  constexpr int kThreads = Cols::kThreads, kSpan = Cols::kSpan, kMost = Ex::kMost, kOwn = NV * E;
+  using XS = UnitSlot<DX, E, MODE, 32, SPAN>;      // dense x
+  using Ex = Exchange<2, SHAPE>;
+  constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kMulti = Cols::kMulti, CL = Cols::kClustered;
+  constexpr int kSpan = SPAN, kMost = Ex::kMost, kOwn = NV * E, kStage = Stage::kBytes;
   static_assert(kDense || MODE != kPhase, "the 8-bit blocks are columns of the matrix: no shift");
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float parts[Ex::kFloats];
-  const Cols cs(p.cols, p.slice, ctas, p.period, p.ldg, p.offset, 8);
+  const Cols cs(p.cols, p.slice, ctas, p.ldg, p.offset, 8);
   Ex ex(parts, ctas);
   const int tid = threadIdx.x, lane = tid & 31;
   const TG* dY = static_cast<const TG*>(p.dY);
   const DX* X = static_cast<const DX*>(p.X);
   const Span gspan = span_of<TG>(p.dY, p.rows, p.cols, p.ldg);
   const Span xspan = span_of<DX>(p.X, p.rows, p.cols, p.ldx);
-  const uint32_t ring0 = smem_u32(ring);
+  const uint32_t ring0 = smem_u32(ring) + (tid >> 5) * (S * kStage);
 
   // row `fetch_row` into the stage at `into`; what a row needs besides, its mean
   // and rstd and the scale codes of its 8-bit blocks, goes into registers one row
@@ -101,30 +98,30 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
   uint32_t into = ring0;
   auto fetch = [&] {
     const bool on = fetch_row < p.rows;
-    if (G < 32 || on) {
+    if (SPAN < 32 || on) {
       const TG* g = dY + fetch_row * p.ldg;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const uint32_t at = into + i * Ring::kOne;
+        const uint32_t at = into + i * Stage::kOne;
         if constexpr (MODE == kAny)
-          GS::start(at, tid, g + cs.col(i), on ? cs.left(i) : -16, cs.last, gspan);
+          GS::start(at, lane, g + cs.col(i), on ? cs.left(i) : -16, cs.last, gspan);
         else
-          GS::start(at, tid, g + cs.col(i), on && cs.whole(i), on && cs.some(i), gspan);
+          GS::start(at, lane, g + cs.col(i), on && cs.whole(i), on && cs.some(i), gspan);
         if constexpr (kDense) {
           const DX* x = X + fetch_row * p.ldx;
           if constexpr (MODE == kAny)
-            XS::start(at + GS::kBytes, tid, x + cs.col(i), on ? cs.left(i) : -16, cs.last, xspan);
+            XS::start(at + GS::kBytes, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, xspan);
           else
-            XS::start(at + GS::kBytes, tid, x + cs.col(i), on && cs.whole(i), on && cs.some(i), xspan);
+            XS::start(at + GS::kBytes, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), xspan);
         } else {
-          cp_async<E>(at + GS::kBytes + E * tid, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
+          cp_async<E>(at + GS::kBytes + E * lane, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
                       on && cs.left(i) > 0);
         }
       }
     }
     cp_async_commit();
     fetch_row += cs.step;
-    into = into + Ring::kStage == ring0 + S * Ring::kStage ? ring0 : into + Ring::kStage;
+    into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
   };
   float next_mean = 0.f, next_rstd = 0.f;
   uint32_t next_sc[kDense ? 1 : NV];
@@ -149,9 +146,9 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
   uint32_t from = ring0;
   // all threads of a row leave the loop together; with several rows in a warp,
   // all of the warp
-  for (int64_t row = cs.row; G >= 32 ? row < p.rows : row - (lane / G) < p.rows; row += cs.step) {
+  for (int64_t row = cs.row; SPAN == 32 ? row < p.rows : row - (lane / SPAN) < p.rows; row += cs.step) {
     fetch();
-    const bool active = G >= 32 || row < p.rows;
+    const bool active = SPAN == 32 || row < p.rows;
     const float mean = next_mean, rstd = next_rstd;
     uint32_t sc[kDense ? 1 : NV];
     if constexpr (!kDense) {
@@ -161,25 +158,25 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
     fetch_stats(row + cs.step);
     cp_async_wait<S - 1>();
     auto g_unit = [&](int i) {
-      const uint32_t at = from + i * Ring::kOne;
+      const uint32_t at = from + i * Stage::kOne;
       if constexpr (MODE == kAny) {
-        return GS::finish(at, tid, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
+        return GS::finish(at, lane, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
-        Unit<TG, E> u = GS::finish(at, tid);
+        Unit<TG, E> u = GS::finish(at, lane);
         if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
         return u;
       }
     };
     auto x_unit = [&](int i) {
-      const uint32_t at = from + i * Ring::kOne + GS::kBytes;
+      const uint32_t at = from + i * Stage::kOne + GS::kBytes;
       XUnit<TX, E> x;
       if constexpr (!kDense) {
-        lds<E / 4>(at + E * tid, x.w);
+        lds<E / 4>(at + E * lane, x.w);
         x.sc = sc[i];
       } else if constexpr (MODE == kAny) {
-        x.u = XS::finish(at, tid, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+        x.u = XS::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
-        x.u = XS::finish(at, tid);
+        x.u = XS::finish(at, lane);
         if (MODE == kPhase && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
       }
       return x;
@@ -213,20 +210,21 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
     }
     if (p.dX) {
       float c1, c2;
-      if constexpr (G <= 32) {
+      if constexpr (!kMulti) {
         c1 = span_sum<kSpan>(s1);
         c2 = span_sum<kSpan>(s2);
       } else {
         const float s = warp_sums2(s1, s2);
         if ((lane & 15) == 0) ex.put(lane >> 4, s);
         const float* pt = ex.sync();
-        if constexpr (2 * kMost <= 32) {
-          const float t = span_sum<kMost>(lane % kMost < ex.warps() && lane < 2 * kMost ? pt[lane] : 0.f);
+        if constexpr (kMost == 16) {
+          // lanes 0 to 15 have the warps' first sums, 16 to 31 their second
+          const float t = span_sum<16>((lane & 15) < ex.warps ? pt[lane] : 0.f);
           c1 = __shfl_sync(0xFFFFFFFFu, t, 0);
-          c2 = __shfl_sync(0xFFFFFFFFu, t, kMost);
+          c2 = __shfl_sync(0xFFFFFFFFu, t, 16);
         } else {
           float a = 0.f, b = 0.f;
-          for (int k = lane; k < ex.warps(); k += 32) {
+          for (int k = lane; k < ex.warps; k += 32) {
             a += pt[k];
             b += pt[kMost + k];
           }
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
         store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
       }
     }
-    from = from + Ring::kStage == ring0 + S * Ring::kStage ? ring0 : from + Ring::kStage;
+    from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
   cp_async_wait<0>();
   // this CTA's partial sums; the ring's memory is free
@@ -270,12 +268,12 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          if (cs.has(i, j)) gather[(tid / G) * (G * kOwn) + cs.col(i) + j] = a[E * i + j];
+          if (cs.has(i, j)) gather[(tid / SPAN) * (SPAN * kOwn) + cs.col(i) + j] = a[E * i + j];
       __syncthreads();
-      for (int c = tid; c < p.cols; c += kThreads) {
+      for (int c = tid; c < p.cols; c += kLaneThreads) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < Cols::kRows; ++k) s += gather[k * (G * kOwn) + c];
+        for (int k = 0; k < Cols::kRows; ++k) s += gather[k * (SPAN * kOwn) + c];
         part[c] = s;
       }
     } else {
@@ -297,46 +295,44 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_bwd_kernel(NormBwdPara
   }
 }
 
-constexpr int kWideBwdCta = 256 * 32;      // columns of a CTA in a cluster
-
 // Launches, or (occupancy) returns how many CTAs or clusters run at once.
-template <typename TX, typename TG, int G, int NV, int E, int MODE, bool CL>
+template <typename TX, typename TG, int SPAN, int NV, int E, int MODE, int SHAPE>
 int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_sms, cudaStream_t s) {
-  using Cols = NormCols<G, NV, E, MODE, CL>;
-  // three stages where they leave room for a second CTA of 256 threads
-  constexpr int S = BwdRing<TX, TG, G, NV, E, 3, MODE>::kBytes <= 110 * 1024 ? 3 : 2;
-  constexpr int kSmem = BwdRing<TX, TG, G, NV, E, S, MODE>::kBytes;
-  auto* kernel = norm_bwd_kernel<TX, TG, G, NV, E, S, MODE, CL>;
+  using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
+  constexpr int kStage = BwdStage<TX, TG, SPAN, NV, E, MODE>::kBytes;
+  constexpr int kGather = SHAPE == kLanes && Cols::kRows > 1 ? 32 * NV * E * 4 : 0;   // of a warp, when the ring is done
+  // two stages and the CTAs that then fit an SM: three stages take 84.2 us against
+  // 82.8 on 16384 x 4096 bf16, and 150.8 against 129.6 in float32
+  constexpr int S = 2;
+  constexpr int kWarp = S * kStage > kGather ? S * kStage : kGather;
+  auto* kernel = norm_bwd_kernel<TX, TG, SPAN, NV, E, S, MODE, SHAPE>;
+  static NormHeld held;
   NormBwdParams p = params;
-  const int need = p.cols + (MODE == kPhase ? 7 : 0);
-  const int ctas = CL ? norm_cluster(need, kWideBwdCta) : 1;
-  if (CL) p.slice = norm_slice(need, ctas);
-  static std::atomic<uint64_t> done{0};
-  static std::atomic<int> held{0};
-  const int per_sm = norm_occupancy(kernel, Cols::kThreads, kSmem, done, held);
+  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), kBwdWarps);
+  p.slice = plan.slice;
+  const int smem = plan.warps * kWarp;
+  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kBwdWarps) * kWarp);
   if (occupancy) {
-    const int64_t most = imax64(1, static_cast<int64_t>(num_sms) * per_sm / ctas);
+    const int64_t most = imax64(1, static_cast<int64_t>(num_sms) * per_sm / plan.ctas);
     return static_cast<int>(
         norm_blocks(imin64((p.rows + Cols::kRows - 1) / Cols::kRows, most), Cols::kRows, p.period));
   }
-  norm_launch(kernel, parts * ctas, Cols::kThreads, kSmem, ctas, p, s);
+  norm_launch(kernel, parts * plan.ctas, 32 * plan.warps, smem, plan.ctas, p, s);
   return 0;
 }
 
 // E columns a unit, 32 a thread (16 where a row has 64 or fewer).
 template <typename TX, typename TG, int E, int MODE>
 int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cudaStream_t s) {
-  constexpr int NV = 32 / E, G0 = E == 8 ? 4 : 8;
+  constexpr int NV = 32 / E, L = E == 8 ? 4 : 8;
   const int cols = p.cols + (MODE == kPhase ? 7 : 0);
-  if (cols <= 64) return norm_bwd_go<TX, TG, G0, 64 / (G0 * E), E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 128) return norm_bwd_go<TX, TG, G0, 128 / (G0 * E), E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 256) return norm_bwd_go<TX, TG, 8, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 512) return norm_bwd_go<TX, TG, 16, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 1024) return norm_bwd_go<TX, TG, 32, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 2048) return norm_bwd_go<TX, TG, 64, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= 4096) return norm_bwd_go<TX, TG, 128, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  if (cols <= kWideBwdCta) return norm_bwd_go<TX, TG, 256, NV, E, MODE, false>(p, parts, occ, num_sms, s);
-  return norm_bwd_go<TX, TG, 256, NV, E, MODE, true>(p, parts, occ, num_sms, s);
+  if (cols <= 64) return norm_bwd_go<TX, TG, L, 64 / (L * E), E, MODE, kLanes>(p, parts, occ, num_sms, s);
+  if (cols <= 128) return norm_bwd_go<TX, TG, L, 128 / (L * E), E, MODE, kLanes>(p, parts, occ, num_sms, s);
+  if (cols <= 256) return norm_bwd_go<TX, TG, 8, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
+  if (cols <= 512) return norm_bwd_go<TX, TG, 16, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
+  if (cols <= 1024) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
+  if (cols <= kBwdWarps * kWarpCols) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCta>(p, parts, occ, num_sms, s);
+  return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCluster>(p, parts, occ, num_sms, s);
 }
 
 template <typename TX>

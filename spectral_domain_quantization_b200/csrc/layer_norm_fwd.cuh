@@ -38,50 +38,42 @@ struct RowStats {
   }
 };
 
-template <typename T, int G, int NV, int E, int S, int MODE>
-struct FwdRing {
-  using C = NormCols<G, NV, E, MODE, false>;
-  using Slot = UnitSlot<T, E, MODE, C::kThreads, C::kSpan>;
-  static constexpr int kStage = NV * Slot::kBytes;
-  static constexpr int kBytes = S * kStage;
-};
-
-template <typename T, int G, int NV, int E, int S, int MODE, bool SAVE, bool CL>
-__global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdParams p, int ctas) {
-  using Cols = NormCols<G, NV, E, MODE, CL>;
-  using Ring = FwdRing<T, G, NV, E, S, MODE>;
-  using Slot = typename Ring::Slot;
-  constexpr bool kRest = sizeof(T) == 4;
-  using Ex = Exchange<G, kRest ? 3 : 2, CL>;
-  constexpr int kThreads = Cols::kThreads, kSpan = Cols::kSpan, kMost = Ex::kMost;
+template <typename T, int SPAN, int NV, int E, int S, int MODE, bool SAVE, int SHAPE>
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd_kernel(NormFwdParams p, int ctas) {
+  using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
+  using Slot = UnitSlot<T, E, MODE, 32, SPAN>;
+  constexpr bool kRest = sizeof(T) == 4, CL = Cols::kClustered, kMulti = Cols::kMulti;
+  constexpr int kSpan = SPAN, kStage = NV * Slot::kBytes;
+  using Ex = Exchange<kRest ? 3 : 2, SHAPE>;
+  constexpr int kMost = Ex::kMost;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float parts[Ex::kFloats];
-  const Cols cs(p.cols, p.slice, ctas, p.period, p.ldx, p.offset, 8);
+  const Cols cs(p.cols, p.slice, ctas, p.ldx, p.offset, 8);
   Ex ex(parts, ctas);
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int lane = threadIdx.x & 31;
   const T* X = static_cast<const T*>(p.X);
   const Span span = span_of<T>(p.X, p.rows, p.cols, p.ldx);
-  const uint32_t ring0 = smem_u32(ring);
+  const uint32_t ring0 = smem_u32(ring) + (threadIdx.x >> 5) * (S * kStage);
 
   // row `fetch_row` into the stage at `into`
   int64_t fetch_row = cs.row;
   uint32_t into = ring0;
   auto fetch = [&] {
     const bool on = fetch_row < p.rows;
-    if (G < 32 || on) {
+    if (SPAN < 32 || on) {
       const T* x = X + fetch_row * p.ldx;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint32_t at = into + i * Slot::kBytes;
         if constexpr (MODE == kAny)
-          Slot::start(at, tid, x + cs.col(i), on ? cs.left(i) : -16, cs.last, span);
+          Slot::start(at, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, span);
         else
-          Slot::start(at, tid, x + cs.col(i), on && cs.whole(i), on && cs.some(i), span);
+          Slot::start(at, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), span);
       }
     }
     cp_async_commit();
     fetch_row += cs.step;
-    into = into + Ring::kStage == ring0 + Ring::kBytes ? ring0 : into + Ring::kStage;
+    into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
   };
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch();
@@ -90,31 +82,25 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
   load_vector(cs, p.b, p.w_dtype, 0.f, b);
   // columns of a warp of the row, as the exchange numbers them
   auto columns_of = [&](int warp) {
-    const int r = CL ? warp / Ex::kWarps : 0;
-    const int shift = MODE == kPhase ? (CL ? static_cast<int>(cluster_rank()) * p.slice : 0) + cs.t * E - cs.c0 : 0;
-    const int b0 = (CL ? r * p.slice : 0) - shift;
-    const int e0 = CL ? min(p.cols, b0 + p.slice) : p.cols, l0 = max(b0, 0);
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = b0 + (i * G + (warp % Ex::kWarps) * 32) * E;
-      n += max(min(e0, at + E * kSpan) - max(l0, at), 0);
-    }
-    return static_cast<float>(n);
+    if constexpr (!kMulti) return static_cast<float>(p.cols);
+    const int per = blockDim.x >> 5;
+    const int b0 = (CL ? warp / per * p.slice : 0) - cs.shift, at = b0 + (CL ? warp % per : warp) * kWarpCols;
+    return static_cast<float>(max(min(CL ? min(p.cols, b0 + p.slice) : p.cols, at + kWarpCols) - max(at, 0), 0));
   };
-  const float n_w = columns_of(G > 32 ? (CL ? static_cast<int>(cluster_rank()) * Ex::kWarps : 0) + (tid >> 5) : 0);
+  const float n_w = columns_of(kMulti ? ex.mine() : 0);
   const float inv_w = n_w > 0.f ? __fdiv_rn(1.f, n_w) : 0.f;
   const float inv_n = __fdiv_rn(1.f, static_cast<float>(p.cols));
-  const float lane_n = G > 32 && lane < ex.warps() ? columns_of(lane) : 0.f;
+  const float lane_n = kMulti && lane < ex.warps ? columns_of(lane) : 0.f;
   const float inv_lane = lane_n > 0.f ? __fdiv_rn(1.f, lane_n) : 0.f;
+  const float n_0 = columns_of(0), inv_0 = __fdiv_rn(1.f, n_0);
   float top = 0.f;
   if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
   uint32_t from = ring0;
   // all threads of a row leave the loop together; with several rows in a warp,
   // all of the warp
-  for (int64_t row = cs.row; G >= 32 ? row < p.rows : row - (lane / G) < p.rows; row += cs.step) {
+  for (int64_t row = cs.row; SPAN == 32 ? row < p.rows : row - (lane / SPAN) < p.rows; row += cs.step) {
     fetch();
-    const bool active = G >= 32 || row < p.rows;
+    const bool active = SPAN == 32 || row < p.rows;
     cp_async_wait<S - 1>();
     float v[NV * E], part[NV];
     Unit<T, E> kept[MODE == kAny && SAVE ? NV : 1];
@@ -123,10 +109,10 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
       const uint32_t at = from + i * Slot::kBytes;
       Unit<T, E> u;
       if constexpr (MODE == kAny) {
-        u = Slot::finish(at, tid, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+        u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
         if constexpr (SAVE) kept[i] = u;
       } else {
-        u = Slot::finish(at, tid);
+        u = Slot::finish(at, lane);
         if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
       }
       u.get(v + E * i);
@@ -156,7 +142,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
     float sq = tree_sum<NV>(p2), rest = 0.f;
     if constexpr (kRest) rest = tree_sum<NV>(p1);
     RowStats st;
-    if constexpr (G <= 32) {
+    if constexpr (!kMulti) {
       sq = span_sum<kSpan>(sq);
       const float r = kRest ? sum_rest(m, n_w, span_sum<kSpan>(rest), sq) : division_rest(m, n_w, sum);
       st.set(m, r * inv_n, fmaf(-r, r * inv_n, sq), inv_n, p.eps);
@@ -178,7 +164,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
       }
       const float* pt = ex.sync();
       // warp k's mean relative to the first's, what it lost (mr; r times its columns)
-      const float first = divide(pt[0], columns_of(0), __fdiv_rn(1.f, columns_of(0)));
+      const float first = divide(pt[0], n_0, inv_0);
       auto dev = [&](int k, float cw, float inv, float& r, float& mr) {
         const float mk = divide(pt[k], cw, inv);
         r = kRest ? pt[2 * kMost + k] : division_rest(mk, cw, pt[k]);
@@ -196,7 +182,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
         st.off = __shfl_sync(0xFFFFFFFFu, st.off, 0);
         st.rstd = __shfl_sync(0xFFFFFFFFu, st.rstd, 0);
       } else {
-        const int nw = ex.warps();
+        const int nw = ex.warps;
         float s = 0.f, x = 0.f;
         for (int k = lane; k < nw; k += 32) {
           const float cw = columns_of(k);
@@ -213,7 +199,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
         st.set(first, shift, span_sum<32>(x), inv_n, p.eps);
       }
     }
-    if (active && cs.t == 0 && (!CL || cluster_rank() == 0)) {
+    if (active && cs.t == 0 && (!kMulti || ex.mine() == 0)) {
       if (p.mean) p.mean[row] = st.mean;
       if (p.rstd) p.rstd[row] = st.rstd;
     }
@@ -232,7 +218,7 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
         if constexpr (MODE == kAny)
           u = kept[i];
         else
-          u = Slot::finish(from + i * Slot::kBytes, tid);
+          u = Slot::finish(from + i * Slot::kBytes, lane);
         float x[E];
         u.get(x);
         uint32_t codes[E / 4];
@@ -250,69 +236,60 @@ __global__ void __launch_bounds__(norm_threads<G>()) norm_fwd_kernel(NormFwdPara
         }
       }
     }
-    from = from + Ring::kStage == ring0 + Ring::kBytes ? ring0 : from + Ring::kStage;
+    from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
   cp_async_wait<0>();
   if constexpr (SAVE) {
-    __shared__ float wm[kThreads / 32];
+    __shared__ float wm[16];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-    if (lane == 0) wm[tid >> 5] = top;
+    if (lane == 0) wm[threadIdx.x >> 5] = top;
     __syncthreads();
     top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, wm[i]);
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) top = fmaxf(top, wm[i]);
     act8_write_amax(p.save.amax,
                     p.save.fmt == METIS_MXINT8 ? act8_held<METIS_MXINT8>(top) : act8_held<METIS_MXFP8>(top));
   }
 }
 
-constexpr int kWideCta = 512 * 32;      // columns of a CTA in a cluster
+constexpr int kFwdWarps = 16;       // of a CTA
 
-template <typename T, int G, int NV, int E, int MODE, bool SAVE, bool CL>
+template <typename T, int SPAN, int NV, int E, int MODE, bool SAVE, int SHAPE>
 void norm_fwd_go(const NormFwdParams& params, int num_sms, cudaStream_t s) {
-  using Cols = NormCols<G, NV, E, MODE, CL>;
-  constexpr int S = 3;
-  constexpr int kSmem = FwdRing<T, G, NV, E, S, MODE>::kBytes;
-  auto* kernel = norm_fwd_kernel<T, G, NV, E, S, MODE, SAVE, CL>;
-  static std::atomic<uint64_t> done{0};
-  static std::atomic<int> held{0};
-  const int per_sm = norm_occupancy(kernel, Cols::kThreads, kSmem, done, held);
+  using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
+  constexpr int S = SHAPE == kLanes ? 3 : 2, kWarp = S * NV * UnitSlot<T, E, MODE, 32, SPAN>::kBytes;
+  auto* kernel = norm_fwd_kernel<T, SPAN, NV, E, S, MODE, SAVE, SHAPE>;
+  static NormHeld held;
   NormFwdParams p = params;
-  const int need = p.cols + (MODE == kPhase ? 7 : 0);
-  const int ctas = CL ? norm_cluster(need, kWideCta) : 1;
-  if (CL) p.slice = norm_slice(need, ctas);
-  const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX) / ctas;
+  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), kFwdWarps);
+  p.slice = plan.slice;
+  const int smem = plan.warps * kWarp;
+  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kFwdWarps) * kWarp);
+  const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX) / plan.ctas;
   const int64_t blocks = imin64((p.rows + Cols::kRows - 1) / Cols::kRows, imax64(1, most));
-  norm_launch(kernel, static_cast<int>(norm_blocks(blocks, Cols::kRows, p.period)) * ctas, Cols::kThreads, kSmem, ctas,
-              p, s);
+  norm_launch(kernel, static_cast<int>(norm_blocks(blocks, Cols::kRows, p.period)) * plan.ctas, 32 * plan.warps, smem,
+              plan.ctas, p, s);
 }
 
 // E columns a unit, 32 a thread (16 where a row has 64 or fewer).
 template <typename T, int E, int MODE, bool SAVE>
 void norm_fwd_cols(const NormFwdParams& p, int num_sms, cudaStream_t s) {
-  constexpr int NV = 32 / E, G0 = E == 8 ? 4 : 8;      // a block of 32 columns lies in 32 / E lanes
+  constexpr int NV = 32 / E, L = E == 8 ? 4 : 8;      // a block of 32 columns lies in 32 / E lanes
   const int cols = p.cols + (MODE == kPhase ? 7 : 0);
   if (cols <= 64)
-    norm_fwd_go<T, G0, 64 / (G0 * E), E, MODE, SAVE, false>(p, num_sms, s);
+    norm_fwd_go<T, L, 64 / (L * E), E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 128)
-    norm_fwd_go<T, G0, 128 / (G0 * E), E, MODE, SAVE, false>(p, num_sms, s);
+    norm_fwd_go<T, L, 128 / (L * E), E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 256)
-    norm_fwd_go<T, 8, NV, E, MODE, SAVE, false>(p, num_sms, s);
+    norm_fwd_go<T, 8, NV, E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 512)
-    norm_fwd_go<T, 16, NV, E, MODE, SAVE, false>(p, num_sms, s);
+    norm_fwd_go<T, 16, NV, E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 1024)
-    norm_fwd_go<T, 32, NV, E, MODE, SAVE, false>(p, num_sms, s);
-  else if (cols <= 2048)
-    norm_fwd_go<T, 64, NV, E, MODE, SAVE, false>(p, num_sms, s);
-  else if (cols <= 4096)
-    norm_fwd_go<T, 128, NV, E, MODE, SAVE, false>(p, num_sms, s);
-  else if (cols <= 8192)
-    norm_fwd_go<T, 256, NV, E, MODE, SAVE, false>(p, num_sms, s);
-  else if (cols <= kWideCta)
-    norm_fwd_go<T, 512, NV, E, MODE, SAVE, false>(p, num_sms, s);
+    norm_fwd_go<T, 32, NV, E, MODE, SAVE, kLanes>(p, num_sms, s);
+  else if (cols <= kFwdWarps * kWarpCols)
+    norm_fwd_go<T, 32, NV, E, MODE, SAVE, kCta>(p, num_sms, s);
   else
-    norm_fwd_go<T, 512, NV, E, MODE, SAVE, true>(p, num_sms, s);
+    norm_fwd_go<T, 32, NV, E, MODE, SAVE, kCluster>(p, num_sms, s);
 }
 
 }  // namespace metis
