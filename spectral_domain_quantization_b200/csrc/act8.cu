@@ -16,10 +16,11 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// unit -> (row, unit in the row): a multiplication by a rounded-up reciprocal
-// for fewer than 2^31 units (Granlund and Montgomery's division by an invariant:
-// with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
-// (mulhi(n, m) + n) >> s), a 64-bit division otherwise.
+// Where unit u of 8 (or E) columns lies.  The codes of all rows form one sequence of
+// units, 4 to a block; a row's first and last element need its row and place: a
+// multiplication by a rounded-up reciprocal for fewer than 2^31 units (Granlund and
+// Montgomery's division by an invariant: with s = ceil(log2 d) and m = floor(2^32
+// (2^s - d) / d) + 1, n / d is (mulhi(n, m) + n) >> s), a 64-bit division otherwise.
 struct UnitMap {
   int64_t total;
   int64_t per_row;
@@ -48,6 +49,19 @@ UnitMap unit_map(int64_t rows, int64_t per_row) {
   return m;
 }
 
+// How a dense matrix lies against the units.
+enum UnitShape {
+  kFlat = 0,      // rows of whole blocks, one behind the other: unit u is elements 8 u to 8 u + 7
+  kRowsAligned,   // rows on 16-byte boundaries
+  kRowsAny
+};
+
+// Columns of a unit of the way back.
+template <typename T>
+constexpr int restore_width(int shape) {
+  return sizeof(T) == 4 && shape != kRowsAny ? 4 : 8;
+}
+
 MDEV float cta_max(float m) {
   __shared__ float wm[kThreads / 32];
 #pragma unroll
@@ -60,12 +74,13 @@ MDEV float cta_max(float m) {
   return m;
 }
 
-// 8 elements a thread, a block in 4 adjacent lanes.  The units of all rows form
-// one sequence (a row's are a multiple of 4), dealt to the lanes in order.
-template <int FMT, typename T, bool AL>
+// 8 elements a thread, a block in 4 adjacent lanes, the units dealt to the lanes in
+// order.
+template <int FMT, typename T, int SHAPE>
 __global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t rows, int64_t cols, int64_t ld,
                                                              Act8View out, UnitMap map) {
-  constexpr int kU = sizeof(T) == 2 ? 4 : 2;      // units in flight per thread
+  constexpr bool AL = SHAPE != kRowsAny;
+  constexpr int kU = 4;                           // units in flight per thread
   const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   const Span span = span_of<T>(X, rows, cols, ld);
@@ -74,79 +89,106 @@ __global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t
   for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
        u0 += kU * stride) {
     UnitLoad<T, AL> in[kU];
-    int64_t row[kU];
-    int k[kU], left[kU];
+    int left[kU];
     bool last[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int64_t u = u0 + i * stride;
-      row[i] = 0;
-      k[i] = 0;
-      left[i] = -16;
-      if (u < map.total) {
-        map.split(u, row[i], k[i]);
-        left[i] = static_cast<int>(cols) - 8 * k[i];
+      const T* src = X + 8 * u;
+      left[i] = 8;
+      last[i] = true;
+      if constexpr (SHAPE != kFlat) {
+        int64_t row;
+        int k;
+        map.split(u < map.total ? u : 0, row, k);
+        left[i] = static_cast<int>(cols) - 8 * k;
+        last[i] = lane == 31 || k + 1 == map.per_row;
+        src = X + row * ld + 8 * k;
       }
-      last[i] = lane == 31 || k[i] + 1 == map.per_row;
-      in[i].start(X + row[i] * ld + 8 * k[i], left[i], last[i], span);
+      if (u >= map.total) left[i] = -16;
+      in[i].start(src, left[i], last[i], span);
     }
+    float v[kU][8];
+    uint32_t codes[kU][2];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) in[i].finish(left[i], last[i]).get(v[i]);
+    const uint32_t sc = act8_blocks<FMT, 8, kU>(v, codes, top);
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const bool mine = u0 + i * stride < map.total;
-      const Unit<T> x = in[i].finish(left[i], last[i]);
-      float v[8];
-      x.get(v);
-      uint32_t codes[2];
-      const uint32_t sc = act8_block<FMT, 8>(v, codes, top);
-      if (mine) {
-        *reinterpret_cast<uint2*>(out.codes + row[i] * out.ldc + 8 * k[i]) = make_uint2(codes[0], codes[1]);
-        if ((k[i] & 3) == 0) out.scales[row[i] * out.blocks + (k[i] >> 2)] = static_cast<uint8_t>(sc);
-      }
+      const int64_t u = u0 + i * stride;
+      if (u < map.total) *reinterpret_cast<uint2*>(out.codes + 8 * u) = make_uint2(codes[i][0], codes[i][1]);
     }
+    const int64_t mine = u0 + (lane & 3) * stride;     // in the block whose scale this lane has
+    if (mine < map.total) out.scales[mine >> 2] = static_cast<uint8_t>(sc);
   }
   act8_write_amax(out.amax, act8_held<FMT>(cta_max(top)));
 }
 
-// 8 elements a thread, as in act8_save_kernel; a row's units stop at its last
-// column.
-template <int FMT, typename T, bool AL>
+// E elements a thread (8, and 4 of an aligned float32 matrix, so that the warp's
+// stores are contiguous); a row's units stop at its last column.
+template <int FMT, typename T, int SHAPE>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View in, int64_t cols, T* Y, int64_t ld,
                                                                 UnitMap map) {
-  constexpr int kU = 4;
+  constexpr int E = restore_width<T>(SHAPE);
+  constexpr int kU = 32 / E;
   const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
        u0 += kU * stride) {
-    uint2 raw[kU];
+    uint32_t raw[kU][E / 4];
     uint32_t sc[kU];
-    int64_t row[kU];
+    T* dst[kU];
     int k[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int64_t u = u0 + i * stride;
-      row[i] = 0;
       k[i] = 0;
-      raw[i] = make_uint2(0u, 0u);
       sc[i] = 0u;
+#pragma unroll
+      for (int w = 0; w < E / 4; ++w) raw[i][w] = 0u;
+      dst[i] = Y + E * u;
       if (u < map.total) {
-        map.split(u, row[i], k[i]);
-        raw[i] = *reinterpret_cast<const uint2*>(in.codes + row[i] * in.ldc + 8 * k[i]);
-        sc[i] = in.scales[row[i] * in.blocks + (k[i] >> 2)];
+        int64_t c = u;                        // the unit's place among the codes'
+        if constexpr (SHAPE != kFlat) {
+          int64_t row;
+          map.split(u, row, k[i]);
+          c = row * (in.ldc / E) + k[i];
+          dst[i] = Y + row * ld + E * k[i];
+        }
+        if constexpr (E == 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(in.codes + 8 * c);
+          raw[i][0] = q.x;
+          raw[i][E / 4 - 1] = q.y;
+        } else {
+          raw[i][0] = *reinterpret_cast<const uint32_t*>(in.codes + 4 * c);
+        }
+        sc[i] = in.scales[c / (32 / E)];
       }
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const float f = act8_factor<FMT>(sc[i]);
-      float v[8];
-      act8_elems4<FMT>(raw[i].x, v);
-      act8_elems4<FMT>(raw[i].y, v + 4);
+      float v[E];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f;
-      Unit<T> y;
+      for (int w = 0; w < E / 4; ++w) act8_elems4<FMT>(raw[i][w], v + 4 * w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= f;
+      Unit<T, E> y;
       y.put(v);
-      const int left = u0 + i * stride < map.total ? static_cast<int>(cols) - 8 * k[i] : 0;
-      store_unit<T, AL>(Y + row[i] * ld + 8 * k[i], y, left, lane == 0 || k[i] == 0,
-                        lane == 31 || k[i] + 1 == map.per_row);
+      const bool on = u0 + i * stride < map.total;
+      if constexpr (SHAPE == kRowsAny) {
+        store_unit<T, false>(dst[i], y, on ? static_cast<int>(cols) - 8 * k[i] : 0, lane == 0 || k[i] == 0,
+                             lane == 31 || k[i] + 1 == map.per_row);
+      } else if (on) {
+        const int left = static_cast<int>(cols) - E * k[i];
+        if (SHAPE == kFlat || left >= E) {
+          y.store(dst[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (j < left) dst[i][j] = y.elem(j);
+        }
+      }
     }
   }
 }
@@ -164,38 +206,46 @@ int grid_for(int per_sm, int64_t ctas, int num_sms) {
   return static_cast<int>(imax64(1, imin64(ctas, most)));
 }
 
-template <int FMT, typename T, bool AL>
-void save_al(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
+template <typename T>
+UnitShape unit_shape(const T* p, int64_t cols, int64_t ld) {
+  if ((reinterpret_cast<uintptr_t>(p) & 15u) || (ld * static_cast<int64_t>(sizeof(T))) % 16) return kRowsAny;
+  return cols % 32 == 0 && ld == cols ? kFlat : kRowsAligned;
+}
+
+template <int FMT, typename T, int SHAPE>
+void save_shape(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
   const UnitMap map = unit_map(rows, 4 * out.blocks);
-  auto* kernel = act8_save_kernel<FMT, T, AL>;
+  auto* kernel = act8_save_kernel<FMT, T, SHAPE>;
   static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
   kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(X, rows, cols, ld, out,
                                                                                              map);
 }
 
-template <int FMT, typename T, bool AL>
-void restore_al(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
-  const UnitMap map = unit_map(rows, (cols + 7) / 8);
-  auto* kernel = act8_restore_kernel<FMT, T, AL>;
+template <int FMT, typename T, int SHAPE>
+void restore_shape(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
+  constexpr int E = restore_width<T>(SHAPE);
+  const UnitMap map = unit_map(rows, (cols + E - 1) / E);
+  auto* kernel = act8_restore_kernel<FMT, T, SHAPE>;
   static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
   kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(in, cols, Y, ld, map);
 }
 
-template <typename T>
-bool aligned_rows(const T* p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
-}
-
 template <int FMT, typename T>
 void save_t(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8View& out, int num_sms, cudaStream_t s) {
-  aligned_rows(X, ld) ? save_al<FMT, T, true>(X, rows, cols, ld, out, num_sms, s)
-                      : save_al<FMT, T, false>(X, rows, cols, ld, out, num_sms, s);
+  switch (unit_shape(X, cols, ld)) {
+    case kFlat: return save_shape<FMT, T, kFlat>(X, rows, cols, ld, out, num_sms, s);
+    case kRowsAligned: return save_shape<FMT, T, kRowsAligned>(X, rows, cols, ld, out, num_sms, s);
+    default: return save_shape<FMT, T, kRowsAny>(X, rows, cols, ld, out, num_sms, s);
+  }
 }
 
 template <int FMT, typename T>
 void restore_t(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t ld, int num_sms, cudaStream_t s) {
-  aligned_rows(Y, ld) ? restore_al<FMT, T, true>(in, rows, cols, Y, ld, num_sms, s)
-                      : restore_al<FMT, T, false>(in, rows, cols, Y, ld, num_sms, s);
+  switch (unit_shape(Y, cols, ld)) {
+    case kFlat: return restore_shape<FMT, T, kFlat>(in, rows, cols, Y, ld, num_sms, s);
+    case kRowsAligned: return restore_shape<FMT, T, kRowsAligned>(in, rows, cols, Y, ld, num_sms, s);
+    default: return restore_shape<FMT, T, kRowsAny>(in, rows, cols, Y, ld, num_sms, s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -226,6 +276,63 @@ struct Act8QuantParams {
 //    scales (the 8-bit blocks run along the columns) come as one byte a lane
 //    for 8 rows, by shuffle.  The codes of a column are put together in shared
 //    memory and leave as contiguous 64 (NVFP4) or 128 bytes a column.
+// a / b, correctly rounded, from b's correctly rounded reciprocal: the first
+// correction leaves a quotient within a unit in the last place, the second rounds it
+// (Markstein).  b within 2^-90 .. 2^90; a quotient under 2^-9 may be off (its scale
+// code is 0 either way).
+MDEV float divide_exact(float a, float b, float inv) {
+  float q = a * inv;
+  q = fmaf(fmaf(-q, b, a), inv, q);
+  return fmaf(fmaf(-q, b, a), inv, q);
+}
+
+// The scale of an NVFP4 tensor, for its blocks.
+struct NvScale {
+  float s_t, inv;
+  bool plain;       // s_t is out of divide_exact's range
+  MDEV explicit NvScale(float s) {
+    s_t = s;
+    inv = __fdiv_rn(1.f, s);
+    plain = !(s > 0x1p-90f && s < 0x1p90f);
+  }
+  // quant_block_nv_tab's scale code of a block with maximum a
+  MDEV uint32_t code(float a) const {
+    if (plain) return e4m3_code(__fdiv_rn(__fdiv_rn(a, s_t), 6.f));
+    return e4m3_code(divide_exact(divide_exact(a, s_t, inv), 6.f, 1.f / 6.f));
+  }
+};
+
+// One FP4 block's codes (8 a word) and scale code; the bytes of quant_block_nv_tab
+// and quant_block_mx.
+template <int FMT4>
+MDEV uint32_t fp4_block(const float* v, const NvScale& nv, const float* enc_tab, uint32_t* w) {
+  constexpr int kBlk = FMT4 == METIS_NVFP4 ? 16 : 32;
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < kBlk; ++j) a = fmaxf(a, fabsf(v[j]));
+  uint32_t code;
+  float enc;
+  if (FMT4 == METIS_NVFP4) {
+    code = nv.code(a);
+    enc = enc_tab[code];
+  } else {
+    int se = a == 0.f ? 0 : floor_log2(a) - 2;
+    se = se < -127 ? -127 : se;
+    code = a == 0.f ? 0u : static_cast<uint32_t>(se + 127);
+    enc = pow2f(-se);
+  }
+  const bool none = FMT4 == METIS_NVFP4 ? code == 0u : a == 0.f;
+#pragma unroll
+  for (int k = 0; k < kBlk / 8; ++k) {
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __fmul_rn(v[8 * k + j], enc);
+    w[k] = e2m1_pack8(q);
+    if (none) w[k] = 0u;
+  }
+  return code;
+}
+
 template <int FMT8, int FMT4, int AXIS>
 __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantParams p) {
   constexpr int kBlk = FMT4 == METIS_NVFP4 ? 16 : 32;
@@ -246,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
     if (blockIdx.x == 0 && tid == 0) *p.tensor_scale = s_t;
     __syncthreads();
   }
+  const NvScale nv(s_t);
   const int64_t tiles = p.otiles * p.itiles;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t ot = t / p.itiles;
@@ -267,17 +375,11 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
           for (int j = 0; j < 8; ++j) act8_elems4<FMT8>(w[j], v + 4 * j);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
-          uint64_t pk[2];
-          if (FMT4 == METIS_NVFP4) {
-            sc4[0] = quant_block_nv_tab(v, s_t, enc_tab, pk[0]);
-            sc4[1] = quant_block_nv_tab(v + 16, s_t, enc_tab, pk[1]);
-          } else {
-            float unused;
-            sc4[0] = quant_block_mx(v, pk, unused);
-          }
-          *reinterpret_cast<uint4*>(p.codes + o * (p.inner / 2) + c / 2) =
-              make_uint4(static_cast<uint32_t>(pk[0]), static_cast<uint32_t>(pk[0] >> 32),
-                         static_cast<uint32_t>(pk[1]), static_cast<uint32_t>(pk[1] >> 32));
+          uint32_t pk[4];
+#pragma unroll
+          for (int b2 = 0; b2 < 32 / kBlk; ++b2)
+            sc4[b2] = fp4_block<FMT4>(v + kBlk * b2, nv, enc_tab, pk + (kBlk / 8) * b2);
+          *reinterpret_cast<uint4*>(p.codes + o * (p.inner / 2) + c / 2) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           if (p.scales_linear) {
 #pragma unroll
             for (int b2 = 0; b2 < 32 / kBlk; ++b2)
@@ -289,61 +391,50 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
           sc_tile[tc_scale_offset(r, u * (32 / kBlk) + b2, kNb)] = static_cast<uint8_t>(sc4[b2]);
       }
     } else {
-      // outer = columns of X, inner = its rows; warps over the blocks of rows
+      // outer = columns of X, inner = its rows; a warp a block of rows
+      constexpr int kQ = FMT4 == METIS_NVFP4 ? 4 : 2;    // columns whose values are held at once
       const int64_t c = o0 + 4 * lane;                   // this lane's 4 columns
-      {
-        const int b = warp;                              // 8 warps, 8 blocks
-        const int64_t r0 = i0 + b * kBlk;
-        uint32_t sc4 = 0;                                // the 4 columns' scale codes
-        uint32_t pk[4][kBlk / 8] = {};
-        if (r0 < p.inner) {                              // whole blocks: inner is a multiple of 32
-          uint32_t raw[kBlk];
-          uint32_t sb[kBlk / 8];
-          const bool in = c < p.in.ldc;
-          const uint8_t* src = p.in.codes + r0 * p.in.ldc + c;
+      const int64_t r0 = i0 + warp * kBlk;
+      uint32_t sc4 = 0;                                  // the 4 columns' scale codes
+      uint32_t pk[4][kBlk / 8] = {};
+      if (r0 < p.inner) {                                // whole blocks: inner is a multiple of 32
+        uint32_t raw[kBlk];
+        float f[kBlk / 8];                               // row 8 j + lane / 4, 8-bit block lane & 3 of the tile's 4
+        const bool in = c < p.in.ldc;
+        const uint8_t* src = p.in.codes + r0 * p.in.ldc + c;
 #pragma unroll
-          for (int j = 0; j < kBlk; ++j) raw[j] = in ? *reinterpret_cast<const uint32_t*>(src + j * p.in.ldc) : 0u;
-          const int64_t blk = (o0 >> 5) + (lane & 3);
+        for (int j = 0; j < kBlk; ++j) raw[j] = in ? *reinterpret_cast<const uint32_t*>(src + j * p.in.ldc) : 0u;
+        const int64_t blk = (o0 >> 5) + (lane & 3);
+        const uint8_t* sp = p.in.scales + (r0 + (lane >> 2)) * p.in.blocks + blk;
 #pragma unroll
-          for (int j = 0; j < kBlk / 8; ++j)
-            sb[j] = blk < p.in.blocks ? p.in.scales[(r0 + 8 * j + (lane >> 2)) * p.in.blocks + blk] : 0u;
-          float f[kBlk];
+        for (int j = 0; j < kBlk / 8; ++j)
+          f[j] = act8_factor<FMT8>(blk < p.in.blocks ? sp[8 * j * p.in.blocks] : 0u);
 #pragma unroll
-          for (int j = 0; j < kBlk; ++j)
-            f[j] = act8_factor<FMT8>(__shfl_sync(0xFFFFFFFFu, sb[j >> 3], 4 * (j & 7) + (lane >> 3)));
+        for (int q0 = 0; q0 < 4; q0 += kQ) {
+          float v[kQ][kBlk];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[kBlk];
+          for (int j = 0; j < kBlk; ++j) {
+            const float fj = __shfl_sync(0xFFFFFFFFu, f[j >> 3], 4 * (j & 7) + (lane >> 3));
 #pragma unroll
-            for (int j = 0; j < kBlk; ++j) v[j] = __fmul_rn(act8_elem_at<FMT8>(raw[j], q), f[j]);
-            uint32_t code;
-            if (FMT4 == METIS_NVFP4) {
-              uint64_t w;
-              code = quant_block_nv_tab(v, s_t, enc_tab, w);
-              pk[q][0] = static_cast<uint32_t>(w);
-              pk[q][1] = static_cast<uint32_t>(w >> 32);
-            } else {
-              uint64_t w[2];
-              float unused;
-              code = quant_block_mx(v, w, unused);
-              pk[q][0] = static_cast<uint32_t>(w[0]);
-              pk[q][1] = static_cast<uint32_t>(w[0] >> 32);
-              pk[q][2 % (kBlk / 8)] = static_cast<uint32_t>(w[1]);
-              pk[q][3 % (kBlk / 8)] = static_cast<uint32_t>(w[1] >> 32);
-            }
-            if (c + q >= p.outer) code = 0u;             // padding columns: scale 0
-            sc4 |= code << (8 * q);
-            if (p.scales_linear && c + q < p.outer)
-              p.scales_linear[(c + q) * (p.inner / kBlk) + r0 / kBlk] = static_cast<uint8_t>(code);
+            for (int q = 0; q < kQ; ++q) v[q][j] = __fmul_rn(act8_elem_at<FMT8>(raw[j], q0 + q), fj);
+          }
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            uint32_t code = fp4_block<FMT4>(v[q], nv, enc_tab, pk[q0 + q]);
+            const int64_t cq = c + q0 + q;
+            if (cq >= p.outer) code = 0u;                // padding columns: scale 0
+            sc4 |= code << (8 * (q0 + q));
+            if (p.scales_linear && cq < p.outer)
+              p.scales_linear[cq * (p.inner / kBlk) + r0 / kBlk] = static_cast<uint8_t>(code);
           }
         }
+      }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sc_tile[tc_scale_offset(4 * lane + q, b, kNb)] = static_cast<uint8_t>(sc4 >> (8 * q));
-          uint8_t* dst = code_tile + (32 * q + lane) * kLdc + b * (kBlk / 2);   // column 4 lane + q
+      for (int q = 0; q < 4; ++q) {
+        sc_tile[tc_scale_offset(4 * lane + q, warp, kNb)] = static_cast<uint8_t>(sc4 >> (8 * q));
+        uint8_t* dst = code_tile + (32 * q + lane) * kLdc + warp * (kBlk / 2);   // column 4 lane + q
 #pragma unroll
-          for (int w = 0; w < kBlk / 8; w += 2) *reinterpret_cast<uint2*>(dst + 4 * w) = make_uint2(pk[q][w], pk[q][w + 1]);
-        }
+        for (int w = 0; w < kBlk / 8; w += 2) *reinterpret_cast<uint2*>(dst + 4 * w) = make_uint2(pk[q][w], pk[q][w + 1]);
       }
     }
     __syncthreads();

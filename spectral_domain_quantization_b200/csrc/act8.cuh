@@ -62,10 +62,68 @@ MDEV uint32_t act8_pack4(const float* q, bool clamp) {
   return static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
 }
 
-// A block whose 32 columns lie in 32 / E adjacent lanes, E each (by whole warps):
-// this lane's codes and the scale code.  `top` follows the largest finite
-// maximum; what 8 bits hold of it is the tensor's largest magnitude, since the
-// rounding of a block's maximum grows with the maximum.
+// NV units of E columns a thread, each unit's block of 32 columns in 32 / E
+// adjacent lanes (by whole warps): the units' code words, and the scale code of a
+// block.  `top` follows the largest finite maximum; what 8 bits hold of it is the
+// tensor's largest magnitude, since the rounding of a block's maximum grows with the
+// maximum.
+//
+// With as many units as lanes (NV == 32 / E) the maxima are reduced while they are
+// dealt out: lane t of the group ends with unit t's block, makes its scale alone and
+// hands the factor round, so the per-block work is done once, not in every lane.
+// Returns the scale code of the block of unit t, t the lane in the group.
+template <int E, int NV>
+constexpr bool act8_dealt = NV == 32 / E;
+
+template <int FMT, int E, int NV>
+MDEV uint32_t act8_blocks(const float (*v)[E], uint32_t (*codes)[E / 4], float& top) {
+  constexpr int kL = 32 / E;
+  static_assert(act8_dealt<E, NV>);
+  const int t = threadIdx.x & (kL - 1);
+  float a[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    a[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) a[i] = max_nan(a[i], fabsf(v[i][j]));
+  }
+  // step s: a lane keeps the units whose bit s is its own, and gets their other half
+#pragma unroll
+  for (int n = NV / 2; n > 0; n >>= 1) {
+    const bool up = t & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? a[i + n] : a[i], give = up ? a[i] : a[i + n];
+      a[i] = max_nan(keep, __shfl_xor_sync(0xFFFFFFFFu, give, n));
+    }
+  }
+  float enc;
+  const uint32_t sc = act8_scale<FMT>(a[0], enc);
+  if (sc != 255u) top = fmaxf(top, a[0]);
+  // a block that rounds to 128 (MXINT8) or is not finite takes the careful way
+  const bool odd = sc == 255u || (FMT == METIS_MXINT8 && a[0] * enc > 127.f);
+  const bool careful = __any_sync(0xFFFFFFFFu, odd);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int from = (threadIdx.x & 31 & ~(kL - 1)) + i;
+    const float f = __shfl_sync(0xFFFFFFFFu, enc, from);
+    float q[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) q[j] = v[i][j] * f;
+    if (careful) {
+      const bool none = __shfl_sync(0xFFFFFFFFu, sc, from) == 255u;
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) codes[i][k] = none ? 0u : act8_pack4<FMT>(q + 4 * k, true);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) codes[i][k] = act8_pack4<FMT>(q + 4 * k, false);
+    }
+  }
+  return sc;
+}
+
+// One unit, its block in 32 / E adjacent lanes (by whole warps); every lane gets the
+// scale code.
 template <int FMT, int E>
 MDEV uint32_t act8_block(const float* v, uint32_t* codes, float& top) {
   float a = 0.f;

@@ -29,25 +29,50 @@ struct XBytes<Act8Tag, E, MODE, SPAN> {
 template <typename TX, int E>
 struct XUnit {
   Unit<TX, E> u;
-  MDEV void get(int, float* v) const { u.get(v); }
+  // (x - mean) rstd
+  MDEV void normed(int, float mean, float rstd, float* xh) const {
+    float x[E];
+    u.get(x);
+#pragma unroll
+    for (int j = 0; j < E; ++j) xh[j] = (x[j] - mean) * rstd;
+  }
+  // (x - mean) a + b
+  MDEV void affine(int, float mean, float a, float b, float* y) const {
+    float x[E];
+    u.get(x);
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = fmaf(x[j] - mean, a, b);
+  }
 };
+// 8 bits: an element is a small integer (or E4M3) times the block's power of two,
+// so that x - mean takes one fma.
 template <int E>
 struct XUnit<Act8Tag, E> {
   uint32_t w[E / 4];
   uint32_t sc;      // scale code
-  MDEV void get(int fmt, float* v) const {
+  MDEV void centered(int fmt, float mean, float* d) const {
     float f;
     if (fmt == METIS_MXINT8) {
       f = act8_factor<METIS_MXINT8>(sc);
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXINT8>(w[k], v + 4 * k);
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXINT8>(w[k], d + 4 * k);
     } else {
       f = act8_factor<METIS_MXFP8>(sc);
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXFP8>(w[k], v + 4 * k);
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXFP8>(w[k], d + 4 * k);
     }
 #pragma unroll
-    for (int j = 0; j < E; ++j) v[j] *= f;
+    for (int j = 0; j < E; ++j) d[j] = fmaf(d[j], f, -mean);
+  }
+  MDEV void normed(int fmt, float mean, float rstd, float* xh) const {
+    centered(fmt, mean, xh);
+#pragma unroll
+    for (int j = 0; j < E; ++j) xh[j] *= rstd;
+  }
+  MDEV void affine(int fmt, float mean, float a, float b, float* y) const {
+    centered(fmt, mean, y);
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = fmaf(y[j], a, b);
   }
 };
 
@@ -189,22 +214,22 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float x[E], dy[E];
+      float xh[E], dy[E];
       const XUnit<TX, E> xv = x_unit(i);
       const Unit<TG, E> gv = g_unit(i);
       if constexpr (kKeep) {
         xu[i] = xv;
         gu[i] = gv;
       }
-      xv.get(p.saved.fmt, x);
+      xv.normed(p.saved.fmt, mean, rstd, xh);
       gv.get(dy);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int k = E * i + j;
-        const float xh = (x[j] - mean) * rstd, gk = dy[j] * w[k];
-        s1 = fmaf(gk, xh, s1);
+        const float gk = dy[j] * w[k];
+        s1 = fmaf(gk, xh[j], s1);
         s2 += gk;
-        aw[k] = fmaf(dy[j], xh, aw[k]);
+        aw[k] = fmaf(dy[j], xh[j], aw[k]);
         ab[k] += dy[j];
       }
     }
@@ -239,14 +264,14 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
       for (int i = 0; i < NV; ++i) {
         float x[E], dy[E];
         if constexpr (kKeep) {
-          xu[i].get(p.saved.fmt, x);
+          xu[i].affine(p.saved.fmt, mean, kd, k0, x);
           gu[i].get(dy);
         } else {
-          x_unit(i).get(p.saved.fmt, x);
+          x_unit(i).affine(p.saved.fmt, mean, kd, k0, x);
           g_unit(i).get(dy);
         }
 #pragma unroll
-        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, fmaf(x[j] - mean, kd, k0));
+        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
         store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
       }
     }

@@ -213,26 +213,40 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
         o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
       }
       store_row_unit_any(cs, y, p.y_dtype, o, i, active);
-      if constexpr (SAVE) {
-        Unit<T, E> u;
+    }
+    if constexpr (SAVE) {
+      float x[NV][E];
+      uint32_t codes[NV][E / 4];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
         if constexpr (MODE == kAny)
-          u = kept[i];
+          kept[i].get(x[i]);
         else
-          u = Slot::finish(from + i * Slot::kBytes, lane);
-        float x[E];
-        u.get(x);
-        uint32_t codes[E / 4];
-        const uint32_t sc = p.save.fmt == METIS_MXINT8 ? act8_block<METIS_MXINT8, E>(x, codes, top)
-                                                       : act8_block<METIS_MXFP8, E>(x, codes, top);
-        const int c = cs.col(i);
-        const int pad = CL ? min(static_cast<int>(p.save.ldc), cs.lo + p.slice) : static_cast<int>(p.save.ldc);
-        if (active && c < pad) {
-          uint8_t* dst = p.save.codes + row * p.save.ldc + c;
+          Slot::finish(from + i * Slot::kBytes, lane).get(x[i]);
+      }
+      const int pad = CL ? min(static_cast<int>(p.save.ldc), cs.lo + p.slice) : static_cast<int>(p.save.ldc);
+      uint8_t* scales = p.save.scales + row * p.save.blocks;
+      if constexpr (act8_dealt<E, NV>) {
+        const uint32_t sc = p.save.fmt == METIS_MXINT8 ? act8_blocks<METIS_MXINT8, E, NV>(x, codes, top)
+                                                       : act8_blocks<METIS_MXFP8, E, NV>(x, codes, top);
+        const int c = cs.col(0) + cs.t % (32 / E) * Cols::kStride;     // in the block whose scale this lane has
+        if (active && c < pad) scales[c >> 5] = static_cast<uint8_t>(sc);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const uint32_t sc = p.save.fmt == METIS_MXINT8 ? act8_block<METIS_MXINT8, E>(x[i], codes[i], top)
+                                                         : act8_block<METIS_MXFP8, E>(x[i], codes[i], top);
+          if (active && cs.col(i) < pad && cs.t % (32 / E) == 0) scales[cs.col(i) >> 5] = static_cast<uint8_t>(sc);
+        }
+      }
+      uint8_t* dst = p.save.codes + row * p.save.ldc;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (active && cs.col(i) < pad) {
           if constexpr (E == 8)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+            *reinterpret_cast<uint2*>(dst + cs.col(i)) = make_uint2(codes[i][0], codes[i][1]);
           else
-            *reinterpret_cast<uint32_t*>(dst) = codes[0];
-          if (cs.t % (32 / E) == 0) p.save.scales[row * p.save.blocks + (c >> 5)] = static_cast<uint8_t>(sc);
+            *reinterpret_cast<uint32_t*>(dst + cs.col(i)) = codes[i][0];
         }
       }
     }
