@@ -88,6 +88,7 @@ metis_status metis_act8_quantize_fp4(const metis_act8_tensor* in, int32_t block_
   const int64_t outer = block_axis == 1 ? in->rows : in->cols;
   const int64_t inner = block_axis == 1 ? in->cols : in->rows;
   METIS_TRY(check_fp4(out, outer, inner, out->fmt));
+  if (outer > (int64_t{1} << 36) || inner > (int64_t{1} << 36)) return METIS_ERR_SHAPE;   // tile counts in 32 bits
   if (out->inner_sum) return METIS_ERR_UNSUPPORTED;
   if (!device_is_sm100()) return METIS_ERR_UNSUPPORTED;
   launch_act8_quantize(act8_view(in), in->rows, in->cols, block_axis, out, device_sm_count(),

@@ -5,6 +5,7 @@
 // All three kernels are bound by HBM: a copy moves 2 (bf16) or 4 bytes in and
 // 1 + 1/32 out per element, or the reverse; the FP4 pass reads 1 + 1/32 and
 // writes 1/2 + 1/16 (NVFP4) or 1/2 + 1/32.
+#include "abi_common.h"
 #include "act8.cuh"
 #include "act8.h"
 #include "fp4_block.cuh"
@@ -193,9 +194,9 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View in, int
   }
 }
 
-int occupancy(const void* kernel) {
+int occupancy(const void* kernel, size_t smem = 0) {
   int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) != cudaSuccess || per_sm < 1)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem) != cudaSuccess || per_sm < 1)
     per_sm = 1;
   return per_sm;
 }
@@ -261,7 +262,8 @@ struct Act8QuantParams {
   uint8_t* scales;
   uint8_t* scales_linear;    // optional
   float* tensor_scale;
-  int64_t otiles, itiles;    // tiles over the padded outer and inner indices
+  int otiles, itiles;        // tiles over the padded outer and inner indices
+  int step_o, step_i;        // gridDim.x as outer and inner tiles
 };
 
 // A CTA takes tiles of 128 outer indices x 8 blocks (axis 0) or 128 inner
@@ -333,6 +335,24 @@ MDEV uint32_t fp4_block(const float* v, const NvScale& nv, const float* enc_tab,
   return code;
 }
 
+// The tiles of a CTA: blockIdx.x, blockIdx.x + gridDim.x, ... of otiles rows of
+// itiles, without a division a tile.
+struct Tile {
+  int o, i;           // outer and inner tile
+  MDEV explicit Tile(const Act8QuantParams& p) {
+    o = static_cast<int>(blockIdx.x) / p.itiles;
+    i = static_cast<int>(blockIdx.x) - o * p.itiles;
+  }
+  MDEV void next(const Act8QuantParams& p) {
+    o += p.step_o;
+    i += p.step_i;
+    if (i >= p.itiles) {
+      i -= p.itiles;
+      ++o;
+    }
+  }
+};
+
 template <int FMT8, int FMT4, int AXIS>
 __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantParams p) {
   constexpr int kBlk = FMT4 == METIS_NVFP4 ? 16 : 32;
@@ -354,10 +374,45 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
     __syncthreads();
   }
   const NvScale nv(s_t);
-  const int64_t tiles = p.otiles * p.itiles;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t ot = t / p.itiles;
-    const int64_t o0 = ot * 128, i0 = (t - ot * p.itiles) * kTi;
+  Tile tile(p);
+  // axis 0: a warp's block of kBlk rows x 128 bytes of the next tile is on its way
+  // (cp.async into the warp's own half of a two-stage ring) while it works on the
+  // current one; its scale codes (row 8 j + lane / 4, 8-bit block lane & 3) wait in
+  // registers
+  constexpr int kRows = AXIS == 0 ? kBlk : 8;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const uint32_t mine = smem_u32(ring) + warp * (2 * 128 * kRows);
+  uint32_t sb[kRows / 8], next_sb[kRows / 8];
+  auto fetch = [&](const Tile& t, int stage) {
+    const int64_t r0 = static_cast<int64_t>(t.i) * kTi + warp * kBlk;
+    const bool rows = t.o < p.otiles && r0 < p.inner;     // whole blocks: inner is a multiple of 32
+    const int64_t c = static_cast<int64_t>(t.o) * 128 + 16 * (lane & 7), blk = static_cast<int64_t>(t.o) * 4 + (lane & 3);
+    const uint8_t* src = p.in.codes + (r0 + (lane >> 3)) * p.in.ldc + c;
+    const uint32_t dst = mine + stage * (128 * kRows) + 16 * lane;
+#pragma unroll
+    for (int j = 0; j < kRows / 4; ++j) {
+      cp_async16(dst + 512 * j, src, rows && c < p.in.ldc ? 16 : 0);
+      src += 4 * p.in.ldc;
+    }
+    cp_async_commit();
+    const uint8_t* sp = p.in.scales + (r0 + (lane >> 2)) * p.in.blocks + blk;
+#pragma unroll
+    for (int j = 0; j < kRows / 8; ++j) next_sb[j] = rows && blk < p.in.blocks ? sp[8 * j * p.in.blocks] : 0u;
+  };
+  if constexpr (AXIS == 0) fetch(tile, 0);
+  int stage = 0;
+  for (; tile.o < p.otiles; tile.next(p)) {
+    const int64_t o0 = static_cast<int64_t>(tile.o) * 128, i0 = static_cast<int64_t>(tile.i) * kTi;
+    if constexpr (AXIS == 0) {
+#pragma unroll
+      for (int j = 0; j < kRows / 8; ++j) sb[j] = next_sb[j];
+      // the other stage was read before the last tile's barriers
+      Tile after = tile;
+      after.next(p);
+      fetch(after, stage ^ 1);
+      cp_async_wait<1>();
+      __syncwarp();                       // the warp's lanes read what the others copied
+    }
     if (AXIS == 1) {
       // 512 units of 32 columns: a row's 4 units in adjacent lanes
 #pragma unroll
@@ -398,25 +453,20 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
       uint32_t sc4 = 0;                                  // the 4 columns' scale codes
       uint32_t pk[4][kBlk / 8] = {};
       if (r0 < p.inner) {                                // whole blocks: inner is a multiple of 32
-        uint32_t raw[kBlk];
-        float f[kBlk / 8];                               // row 8 j + lane / 4, 8-bit block lane & 3 of the tile's 4
-        const bool in = c < p.in.ldc;
-        const uint8_t* src = p.in.codes + r0 * p.in.ldc + c;
+        float f[kBlk / 8];
 #pragma unroll
-        for (int j = 0; j < kBlk; ++j) raw[j] = in ? *reinterpret_cast<const uint32_t*>(src + j * p.in.ldc) : 0u;
-        const int64_t blk = (o0 >> 5) + (lane & 3);
-        const uint8_t* sp = p.in.scales + (r0 + (lane >> 2)) * p.in.blocks + blk;
-#pragma unroll
-        for (int j = 0; j < kBlk / 8; ++j)
-          f[j] = act8_factor<FMT8>(blk < p.in.blocks ? sp[8 * j * p.in.blocks] : 0u);
+        for (int j = 0; j < kBlk / 8; ++j) f[j] = act8_factor<FMT8>(sb[j]);
+        const uint32_t at = mine + stage * (128 * kBlk) + 4 * lane;
 #pragma unroll
         for (int q0 = 0; q0 < 4; q0 += kQ) {
           float v[kQ][kBlk];
 #pragma unroll
           for (int j = 0; j < kBlk; ++j) {
+            uint32_t raw;                                // 4 columns of row j
+            lds<1>(at + 128 * j, &raw);
             const float fj = __shfl_sync(0xFFFFFFFFu, f[j >> 3], 4 * (j & 7) + (lane >> 3));
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) v[q][j] = __fmul_rn(act8_elem_at<FMT8>(raw[j], q0 + q), fj);
+            for (int q = 0; q < kQ; ++q) v[q][j] = __fmul_rn(act8_elem_at<FMT8>(raw, q0 + q), fj);
           }
 #pragma unroll
           for (int q = 0; q < kQ; ++q) {
@@ -454,19 +504,27 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
       *reinterpret_cast<uint4*>(p.scales + tc_scale_offset(o0, i0 / kBlk, p.scale_cols) + 16 * tid) =
           *reinterpret_cast<const uint4*>(sc_tile + 16 * tid);
     __syncthreads();
+    stage ^= 1;
   }
+  if constexpr (AXIS == 0) cp_async_wait<0>();
+}
+
+template <int FMT8, int FMT4, int AXIS>
+void quantize_axis(const Act8QuantParams& params, int num_sms, cudaStream_t s) {
+  Act8QuantParams p = params;
+  constexpr int kSmem = AXIS == 0 ? 8 * 2 * 128 * (FMT4 == METIS_NVFP4 ? 16 : 32) : 0;   // the warps' rings
+  auto* kernel = act8_quantize_kernel<FMT8, FMT4, AXIS>;
+  if (AXIS == 0) ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
+  static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel), kSmem);
+  const int grid = grid_for(per_sm, static_cast<int64_t>(p.otiles) * p.itiles, num_sms);
+  p.step_o = grid / p.itiles;
+  p.step_i = grid % p.itiles;
+  kernel<<<grid, kThreads, kSmem, s>>>(p);
 }
 
 template <int FMT8, int FMT4>
 void quantize_t(const Act8QuantParams& p, int axis, int num_sms, cudaStream_t s) {
-  const int64_t tiles = p.otiles * p.itiles;
-  if (axis == 1) {
-    static const int per_sm = occupancy(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 1>));
-    act8_quantize_kernel<FMT8, FMT4, 1><<<grid_for(per_sm, tiles, num_sms), kThreads, 0, s>>>(p);
-  } else {
-    static const int per_sm = occupancy(reinterpret_cast<const void*>(act8_quantize_kernel<FMT8, FMT4, 0>));
-    act8_quantize_kernel<FMT8, FMT4, 0><<<grid_for(per_sm, tiles, num_sms), kThreads, 0, s>>>(p);
-  }
+  axis == 1 ? quantize_axis<FMT8, FMT4, 1>(p, num_sms, s) : quantize_axis<FMT8, FMT4, 0>(p, num_sms, s);
 }
 
 }  // namespace
@@ -512,9 +570,9 @@ void launch_act8_quantize(const Act8View& in, int64_t rows, int64_t cols, int ax
   p.scales = out->scales;
   p.scales_linear = out->scales_linear;
   p.tensor_scale = out->tensor_scale;
-  p.otiles = tc_scale_rows(p.outer) / 128;
+  p.otiles = static_cast<int>(tc_scale_rows(p.outer) / 128);     // (outer < 2^37: checked by the entry point)
   const int blk = out->fmt == METIS_NVFP4 ? 16 : 32;
-  p.itiles = p.scale_cols * blk / (axis == 0 ? 8 * blk : 128);   // the padded scale columns too
+  p.itiles = static_cast<int>(p.scale_cols * blk / (axis == 0 ? 8 * blk : 128));   // the padded scale columns too
   const bool i8 = in.fmt == METIS_MXINT8, nv = out->fmt == METIS_NVFP4;
   if (i8)
     nv ? quantize_t<METIS_MXINT8, METIS_NVFP4>(p, axis, num_sms, s)
