@@ -65,6 +65,13 @@ struct NormCols {
   MDEV bool whole(int i) const {
     return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? col(i) >= lo && col(i) + E <= hi : col(i) + E <= hi);
   }
+  // every unit of the warp (by whole warps)
+  MDEV bool all_whole() const {
+    bool w = true;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w = w && whole(i);
+    return __all_sync(0xFFFFFFFFu, w);
+  }
   MDEV bool has(int i, int j) const { return col(i) + j < hi && (MODE != kPhase || col(i) + j >= lo); }
 };
 
@@ -110,8 +117,9 @@ MDEV void load_vector(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, const void* 
   }
 }
 
-// Unit i of an output row of type TY at `p` (its first column's place).
-template <typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
+// Unit i of an output row of type TY at `p` (its first column's place); kWhole: the
+// unit is known to be whole.
+template <bool kWhole, typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
 MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, const float* v, int i, bool active) {
   if constexpr (MODE == kAny) {
     Unit<TY> u;
@@ -120,9 +128,9 @@ MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, co
   } else {
     Unit<TY, E> u;
     u.put(v);
-    if (active && cs.whole(i)) {
+    if (active && (kWhole || cs.whole(i))) {
       u.store(p);
-    } else if (MODE == kPhase && active && cs.some(i)) {
+    } else if (MODE == kPhase && !kWhole && active && cs.some(i)) {
 #pragma unroll
       for (int j = 0; j < E; ++j)
         if (cs.has(i, j)) p[j] = u.elem(j);
@@ -130,14 +138,14 @@ MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, co
   }
 }
 
-// y: the row's place of column 0, in bytes.
-template <int SPAN, int NV, int E, int MODE, int SHAPE>
+// y: the row's place of column 0.
+template <bool kWhole, int SPAN, int NV, int E, int MODE, int SHAPE>
 MDEV void store_row_unit_any(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, void* y, int dtype, const float* v, int i,
                              bool active) {
   if (dtype == METIS_BF16)
-    store_row_unit(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
+    store_row_unit<kWhole>(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
   else
-    store_row_unit(cs, static_cast<float*>(y) + cs.col(i), v, i, active);
+    store_row_unit<kWhole>(cs, static_cast<float*>(y) + cs.col(i), v, i, active);
 }
 
 // s / n for n's rounded reciprocal: one correction of the product (Markstein),
@@ -164,6 +172,16 @@ MDEV float tree_sum(const float* v) {
   } else {
     return tree_sum<N / 2>(v) + tree_sum<N / 2>(v + N / 2);
   }
+}
+
+// The same of any number of values.
+template <int N>
+MDEV float tree_sum_any(const float* v) {
+  constexpr int kHead = N >= 8 ? 8 : (N >= 4 ? 4 : (N >= 2 ? 2 : 1));
+  if constexpr (N == kHead)
+    return tree_sum<N>(v);
+  else
+    return tree_sum<kHead>(v) + tree_sum_any<N - kHead>(v + kHead);
 }
 
 // Sums over a warp of two values at once: in the first step a lane passes on the

@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
   load_vector(cs, p.w, p.w_dtype, 1.f, w);
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) aw[k] = ab[k] = 0.f;
+  // a second body for warps without a partial unit: 65536 x 1001 takes 130 us with it
+  // against 150; rows of several warps have no registers for it
+  constexpr bool kEasy = MODE == kPhase && !kMulti;
+  const bool easy = kEasy && cs.all_whole();
   if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
   uint32_t from = ring0;
   // all threads of a row leave the loop together; with several rows in a warp,
@@ -182,17 +186,17 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     }
     fetch_stats(row + cs.step);
     cp_async_wait<S - 1>();
-    auto g_unit = [&](int i) {
+    auto g_unit = [&](int i, bool whole) {
       const uint32_t at = from + i * Stage::kOne;
       if constexpr (MODE == kAny) {
         return GS::finish(at, lane, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
         Unit<TG, E> u = GS::finish(at, lane);
-        if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+        if (MODE == kPhase && !whole && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
         return u;
       }
     };
-    auto x_unit = [&](int i) {
+    auto x_unit = [&](int i, bool whole) {
       const uint32_t at = from + i * Stage::kOne + GS::kBytes;
       XUnit<TX, E> x;
       if constexpr (!kDense) {
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
         x.u = XS::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
         x.u = XS::finish(at, lane);
-        if (MODE == kPhase && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
+        if (MODE == kPhase && !whole && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
       }
       return x;
     };
@@ -212,27 +216,33 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     XUnit<TX, E> xu[kKeep ? NV : 1];
     Unit<TG, E> gu[kKeep ? NV : 1];
     float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
+    auto sums = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float xh[E], dy[E];
-      const XUnit<TX, E> xv = x_unit(i);
-      const Unit<TG, E> gv = g_unit(i);
-      if constexpr (kKeep) {
-        xu[i] = xv;
-        gu[i] = gv;
-      }
-      xv.normed(p.saved.fmt, mean, rstd, xh);
-      gv.get(dy);
+      for (int i = 0; i < NV; ++i) {
+        float xh[E], dy[E];
+        const XUnit<TX, E> xv = x_unit(i, decltype(whole)::value);
+        const Unit<TG, E> gv = g_unit(i, decltype(whole)::value);
+        if constexpr (kKeep) {
+          xu[i] = xv;
+          gu[i] = gv;
+        }
+        xv.normed(p.saved.fmt, mean, rstd, xh);
+        gv.get(dy);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int k = E * i + j;
-        const float gk = dy[j] * w[k];
-        s1 = fmaf(gk, xh[j], s1);
-        s2 += gk;
-        aw[k] = fmaf(dy[j], xh[j], aw[k]);
-        ab[k] += dy[j];
+        for (int j = 0; j < E; ++j) {
+          const int k = E * i + j;
+          const float gk = dy[j] * w[k];
+          s1 = fmaf(gk, xh[j], s1);
+          s2 += gk;
+          aw[k] = fmaf(dy[j], xh[j], aw[k]);
+          ab[k] += dy[j];
+        }
       }
-    }
+    };
+    if (kEasy && easy)
+      sums(std::true_type{});
+    else
+      sums(std::false_type{});
     if (p.dX) {
       float c1, c2;
       if constexpr (!kMulti) {
@@ -260,20 +270,26 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
       // dx = rstd g + (x - mean) kd + k0
       const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -rstd * (c2 * p.inv_n);
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
+      auto put = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float x[E], dy[E];
-        if constexpr (kKeep) {
-          xu[i].affine(p.saved.fmt, mean, kd, k0, x);
-          gu[i].get(dy);
-        } else {
-          x_unit(i).affine(p.saved.fmt, mean, kd, k0, x);
-          g_unit(i).get(dy);
+        for (int i = 0; i < NV; ++i) {
+          float x[E], dy[E];
+          if constexpr (kKeep) {
+            xu[i].affine(p.saved.fmt, mean, kd, k0, x);
+            gu[i].get(dy);
+          } else {
+            x_unit(i, decltype(whole)::value).affine(p.saved.fmt, mean, kd, k0, x);
+            g_unit(i, decltype(whole)::value).get(dy);
+          }
+#pragma unroll
+          for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
+          store_row_unit_any<decltype(whole)::value>(cs, out, p.dx_dtype, dy, i, active);
         }
-#pragma unroll
-        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
-        store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
-      }
+      };
+      if (kEasy && easy)
+        put(std::true_type{});
+      else
+        put(std::false_type{});
     }
     from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
   const float lane_n = kMulti && lane < ex.warps ? columns_of(lane) : 0.f;
   const float inv_lane = lane_n > 0.f ? __fdiv_rn(1.f, lane_n) : 0.f;
   const float n_0 = columns_of(0), inv_0 = __fdiv_rn(1.f, n_0);
+  const bool easy = MODE == kPhase && cs.all_whole();
   float top = 0.f;
   if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
   uint32_t from = ring0;
@@ -104,43 +105,50 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
     cp_async_wait<S - 1>();
     float v[NV * E], part[NV];
     Unit<T, E> kept[MODE == kAny && SAVE ? NV : 1];
+float sum, m, p2[NV], p1[NV];
+    auto sums = [&](auto easy) {
+      constexpr bool kEasy = decltype(easy)::value;   // every unit of the warp is whole
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t at = from + i * Slot::kBytes;
-      Unit<T, E> u;
-      if constexpr (MODE == kAny) {
-        u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
-        if constexpr (SAVE) kept[i] = u;
-      } else {
-        u = Slot::finish(at, lane);
-        if (MODE == kPhase && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t at = from + i * Slot::kBytes;
+        Unit<T, E> u;
+        if constexpr (MODE == kAny) {
+          u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+          if constexpr (SAVE) kept[i] = u;
+        } else {
+          u = Slot::finish(at, lane);
+          if (MODE == kPhase && !kEasy && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+        }
+        u.get(v + E * i);
+        part[i] = tree_sum<E>(v + E * i);
       }
-      u.get(v + E * i);
-      part[i] = tree_sum<E>(v + E * i);
-    }
-    const float sum = span_sum<kSpan>(tree_sum<NV>(part));
-    const float m = divide(sum, n_w, inv_w);
-    float p2[NV], p1[NV];
+      sum = span_sum<kSpan>(tree_sum_any<NV>(part));
+      m = divide(sum, n_w, inv_w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[E];
+      for (int i = 0; i < NV; ++i) {
+        float e[E];
 #pragma unroll
-      for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
-      if (MODE != kAligned && !cs.whole(i)) {
+        for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
+        if (MODE != kAligned && !kEasy && !cs.whole(i)) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
-      }
-      p2[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
-      if constexpr (kRest) p1[i] = tree_sum<E>(e);
-      if (MODE == kAligned && !cs.whole(i)) {
+          for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
+        }
         p2[i] = 0.f;
-        if constexpr (kRest) p1[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
+        if constexpr (kRest) p1[i] = tree_sum<E>(e);
+        if (MODE == kAligned && !cs.whole(i)) {
+          p2[i] = 0.f;
+          if constexpr (kRest) p1[i] = 0.f;
+        }
       }
-    }
-    float sq = tree_sum<NV>(p2), rest = 0.f;
-    if constexpr (kRest) rest = tree_sum<NV>(p1);
+    };
+    if (MODE == kPhase && easy)
+      sums(std::true_type{});
+    else
+      sums(std::false_type{});
+    float sq = tree_sum_any<NV>(p2), rest = 0.f;
+    if constexpr (kRest) rest = tree_sum_any<NV>(p1);
     RowStats st;
     if constexpr (!kMulti) {
       sq = span_sum<kSpan>(sq);
@@ -204,16 +212,22 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
       if (p.rstd) p.rstd[row] = st.rstd;
     }
     void* y = static_cast<char*>(p.Y) + row * p.ldy * (p.y_dtype == METIS_BF16 ? 2 : 4);
+    auto put = [&](auto easy) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float o[E];
+      for (int i = 0; i < NV; ++i) {
+        float o[E];
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int k = E * i + j;
-        o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
+        for (int j = 0; j < E; ++j) {
+          const int k = E * i + j;
+          o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
+        }
+        store_row_unit_any<decltype(easy)::value>(cs, y, p.y_dtype, o, i, active);
       }
-      store_row_unit_any(cs, y, p.y_dtype, o, i, active);
-    }
+    };
+    if (MODE == kPhase && easy)
+      put(std::true_type{});
+    else
+      put(std::false_type{});
     if constexpr (SAVE) {
       float x[NV][E];
       uint32_t codes[NV][E / 4];
@@ -285,7 +299,8 @@ void norm_fwd_go(const NormFwdParams& params, int num_sms, cudaStream_t s) {
               plan.ctas, p, s);
 }
 
-// E columns a unit, 32 a thread (16 where a row has 64 or fewer).
+// E columns a unit, 32 a thread (16 where a row has 64 or fewer; 40 or 48 where that
+// saves the row's second warp: 16384 x 1027 bf16 takes 29.5 us so against 48.1).
 template <typename T, int E, int MODE, bool SAVE>
 void norm_fwd_cols(const NormFwdParams& p, int num_sms, cudaStream_t s) {
   constexpr int NV = 32 / E, L = E == 8 ? 4 : 8;      // a block of 32 columns lies in 32 / E lanes
@@ -300,6 +315,10 @@ void norm_fwd_cols(const NormFwdParams& p, int num_sms, cudaStream_t s) {
     norm_fwd_go<T, 16, NV, E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 1024)
     norm_fwd_go<T, 32, NV, E, MODE, SAVE, kLanes>(p, num_sms, s);
+  else if (cols <= 1280)
+    norm_fwd_go<T, 32, 40 / E, E, MODE, SAVE, kLanes>(p, num_sms, s);
+  else if (cols <= 1536)
+    norm_fwd_go<T, 32, 48 / E, E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= kFwdWarps * kWarpCols)
     norm_fwd_go<T, 32, NV, E, MODE, SAVE, kCta>(p, num_sms, s);
   else
