@@ -450,7 +450,7 @@ METIS_API metis_status metis_spectral_scale(const float* G, int64_t K, int64_t N
  *       any alignment of its elements, ld >= cols.
  *   out  host struct with device buffers; out->fmt selects the format, rows and
  *       cols must match.
- * rows may be 0 (then only amax is written).  No workspace.
+ * rows may be 0 (then only amax is written); cols at most 2^30.  No workspace.
  * The pages have no counterpart: training keeps the layer's input for the
  * backward products, and the FP4 path quantizes it again there along the batch.
  * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtype, fmt), METIS_ERR_SHAPE,
@@ -500,8 +500,8 @@ METIS_API metis_status metis_act8_quantize_fp4(const metis_act8_tensor* in, int3
  *   saved   optional (NULL: none): X in 8 bits (metis_act8_tensor, rows x cols),
  *           the bytes metis_act8_save writes, from the same pass over X.
  * X, Y and ld need no more alignment than their elements; rows may be 0.
- * Statistics are float32 sums in a fixed order (the mean is corrected by the
- * mean of the deviations, so a large common offset loses no accuracy).
+ * Statistics are float32 sums in a fixed order; neither the variance nor the
+ * mean of a row far from zero is a difference of large sums.
  * A row with an infinity or a NaN gives NaN in that row alone.  No workspace.
  * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtypes, eps, fmt), METIS_ERR_SHAPE,
  * METIS_ERR_ALIGN, METIS_ERR_UNSUPPORTED, METIS_ERR_CUDA.
@@ -528,7 +528,8 @@ METIS_API metis_status metis_layer_norm_fwd(const void* X, int32_t dtype, int64_
  *   dweight, dbias     device, cols floats each, or NULL (not wanted); written,
  *           not added to.  At least one output is given.
  * rows may be 0: dweight and dbias are then zero.  Sums over the rows are
- * float32, in a fixed order that depends on the sizes and the device alone.
+ * float32, in a fixed order that depends on the sizes, types, alignments and the
+ * device alone.
  * Workspace: partial sums of dweight and dbias.
  * Errors as for metis_layer_norm_fwd, and METIS_ERR_WORKSPACE.
  */

@@ -634,15 +634,18 @@ def _out_matrix(t, name, shape, device):
     return ld
 
 
-def _run_on(device, fn, what, *args):
-    """fn(*args) with `device` current (the library launches on the current
-    device); args end with that device's current stream."""
+def _status_on(device, fn, *args):
+    """fn(*args, stream)'s status with `device` current (the library launches on
+    the current device) and that device's current stream."""
     index = device.index
     if torch.cuda.current_device() == index:
-        _check(fn(*args, _stream_of(index)), what)
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_of(index)), what)
+        return fn(*args, _stream_of(index))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_of(index))
+
+
+def _run_on(device, fn, what, *args):
+    _check(_status_on(device, fn, *args), what)
 
 
 class Act8:
@@ -653,7 +656,8 @@ class Act8:
     = ceil(cols / 32); amax: float32 (ACT8_AMAX), whose largest is the largest
     magnitude held.  Without buffers an empty one is allocated; a program that
     stores an activation elsewhere (host memory, a file) keeps the three
-    tensors and passes them back in."""
+    tensors and passes them back in.  (The tensors may be written to, not
+    replaced.)"""
 
     def __init__(self, fmt, rows, cols, device="cuda", codes=None, scales=None, amax=None):
         if fmt not in ACT8_FMT:
@@ -799,6 +803,8 @@ def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=Non
         ldy = cols
     else:
         ldy = _out_matrix(out, "out", (rows, cols), dev)
+        if out.data_ptr() == X.data_ptr() and rows and (out.dtype != X.dtype or ldy != ldx):
+            raise ValueError("out may be X itself, not another view of its memory")
     saved = None if save is None else Act8(save, rows, cols, dev)
     mean = rstd = mp = rp = None
     if stats:
@@ -809,6 +815,9 @@ def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=Non
             X.data_ptr(), _DTYPE_CODE[X.dtype], rows, cols, ldx, w, b, wdt, eps, out.data_ptr(),
             _DTYPE_CODE[out.dtype], ldy, mp, rp, None if saved is None else ctypes.byref(saved._s))
     return LayerNorm(out, mean, rstd, saved)
+
+
+_norm_ws = {}     # workspace bytes of layer_norm_bwd by device and sizes
 
 
 def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True, want_dw=True, want_db=True,
@@ -846,6 +855,8 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
                 raise TypeError("only bfloat16 and float32 outputs are supported")
         else:
             ldd = _out_matrix(out, "out", (rows, cols), dev)
+            if out.data_ptr() == dY.data_ptr() and rows and (out.dtype != dY.dtype or ldd != ldg):
+                raise ValueError("out may be dY itself, not another view of its memory")
         dp, ddt = out.data_ptr(), _DTYPE_CODE[out.dtype]
     else:
         out = None
@@ -854,12 +865,25 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
     args = (dY.data_ptr(), _DTYPE_CODE[dY.dtype], rows, cols, ldg, xp, xdt, ldx, sp,
             mean.data_ptr() if rows else None, rstd.data_ptr() if rows else None, w, wdt, dp, ddt, ldd,
             None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
+    # The workspace is this call's alone (two threads may call at once); it stays
+    # with the stream's allocator, or with the graph that captures the call.  The
+    # size last asked for with these sizes is tried first: types and alignments may
+    # need more, which the library refuses before anything is launched.
     fn = lib().metis_layer_norm_bwd
-    if torch.cuda.current_device() == dev.index:
-        _call_with_workspace(fn, args, (_stream_of(dev.index),), dev, "metis_layer_norm_bwd")
-    else:
-        with torch.cuda.device(dev):
-            _call_with_workspace(fn, args, (_stream_of(dev.index),), dev, "metis_layer_norm_bwd")
+    key = (dev.index, rows, cols)
+    need = _norm_ws.get(key, 256)
+    for last in (False, True):
+        size = ctypes.c_size_t(need)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        status = _status_on(dev, fn, *args, ws.data_ptr(), ctypes.byref(size))
+        if status != ERR_WORKSPACE or last:
+            _check(status, "metis_layer_norm_bwd")
+            break
+        _check(_status_on(dev, fn, *args, None, ctypes.byref(size)), "metis_layer_norm_bwd (workspace query)")
+        need = size.value
+        if len(_norm_ws) >= 4096:
+            _norm_ws.clear()
+        _norm_ws[key] = need
     return out, dw, db
 
 

@@ -22,8 +22,8 @@ metis_status check_act8(const metis_act8_tensor* t) {
 }
 
 metis_status check_extent(int64_t rows, int64_t cols) {
-  // rows * (padded cols) stays far inside 63 bits
-  if (rows < 0 || cols <= 0 || rows > (int64_t{1} << 40) || cols > INT32_MAX - 64 ||
+  // columns are counted in 32 bits, and rows * (padded cols) stays far inside 63
+  if (rows < 0 || cols <= 0 || rows > (int64_t{1} << 40) || cols > (int64_t{1} << 30) ||
       (rows > 0 && cols > (int64_t{1} << 50) / rows))
     return METIS_ERR_SHAPE;
   return METIS_OK;

@@ -14,6 +14,11 @@ mean(g) a sum each:
   |dw - dw*| <= u (D2 + 4) sum|dy xh|,  |db - db*| <= u D2 sum|dy|
 with D2 the additions a column's sum passes through.  D <= cols / 1024 + 64 and
 D2 <= rows / 16 + 64 for every kernel here."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -270,6 +275,83 @@ def test_other_stream_and_two_graphs():
         assert all(torch.equal(p, q) for p, q in zip(want, o))
 
 
+def test_first_call_in_a_capture():
+    # a fresh process whose first call of each kernel is captured
+    code = (
+        "import torch\n"
+        "from spectral_domain_quantization_b200 import api\n"
+        "X = torch.randn(64, 1000, device='cuda').bfloat16()\n"
+        "w = torch.ones(1000, device='cuda')\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    r = api.layer_norm_fwd(X, w, save='mxint8')\n"
+        "    d = api.layer_norm_bwd(X, r.saved, r.mean, r.rstd, w)\n"
+        "    q = api.quantize_fp4_act8(r.saved, 'mx', axis=0)\n"
+        "g.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "r2 = api.layer_norm_fwd(X, w, save='mxint8')\n"
+        "d2 = api.layer_norm_bwd(X, r2.saved, r2.mean, r2.rstd, w)\n"
+        "q2 = api.quantize_fp4_act8(r2.saved, 'mx', axis=0)\n"
+        "assert torch.equal(r.Y, r2.Y) and all(torch.equal(a, b) for a, b in zip(d, d2))\n"
+        "assert torch.equal(q.codes, q2.codes) and torch.equal(q.scales, q2.scales) and float(q.tensor_scale) == 1\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
+
+
+def test_two_threads_on_one_stream():
+    cases = []
+    for k in range(2):
+        x, dy, w, _ = data(3000, 520, seed=20 + k)
+        X, dY, w = mat(x, "bf16"), mat(dy, "bf16"), w.cuda()
+        r = api.layer_norm_fwd(X, w)
+        cases.append((dY, X, r.mean, r.rstd, w))
+    want = [api.layer_norm_bwd(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(k):
+        for _ in range(200):
+            got[k].append(api.layer_norm_bwd(*cases[k])[1:])
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert len(got[k]) == 200
+        for dw, db in got[k]:
+            assert torch.equal(dw, want[k][1]) and torch.equal(db, want[k][2])
+
+
+def test_offsets_past_32_bits():
+    # 2.3e9 elements: the rows at the end against the same rows alone
+    rows, cols, tail = 70000, 32768, 40
+    X = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    X.normal_(generator=torch.Generator(device="cuda").manual_seed(11))
+    w = 1 + 0.1 * torch.randn(cols, device="cuda")
+    r = api.layer_norm_fwd(X, w, w, save="mxint8")
+    t = api.layer_norm_fwd(X[-tail:].clone(), w, w, save="mxint8")
+    assert torch.equal(r.Y[-tail:], t.Y) and torch.equal(r.mean[-tail:], t.mean)
+    assert torch.equal(r.saved.codes[-tail:], t.saved.codes) and torch.equal(r.saved.scales[-tail:], t.saved.scales)
+    a = api.save_act8(X)
+    assert torch.equal(a.codes, r.saved.codes) and torch.equal(a.scales, r.saved.scales)
+    del r.Y
+    out = api.restore_act8(a)
+    assert torch.equal(out[-tail:], api.restore_act8(t.saved))
+    dX = api.layer_norm_bwd(X, a, r.mean, r.rstd, w, want_dw=False, want_db=False, out=out)[0]
+    assert torch.equal(dX[-tail:], api.layer_norm_bwd(X[-tail:].clone(), t.saved, t.mean, t.rstd, w)[0])
+    rows = rows // 32 * 32
+    b = api.Act8("mxint8", rows, cols, codes=a.codes[:rows], scales=a.scales[:rows], amax=a.amax)
+    q = api.quantize_fp4_act8(b, "nv", axis=1)
+    c = api.Act8("mxint8", 32, cols, codes=a.codes[rows - 32:rows], scales=a.scales[rows - 32:rows], amax=a.amax)
+    assert torch.equal(q.codes[-16 * cols:], api.quantize_fp4_act8(c, "nv", axis=1).codes)
+    q = api.quantize_fp4_act8(b, "nv", axis=0).codes.view(cols, rows // 2)
+    assert torch.equal(q[:, -16:], api.quantize_fp4_act8(c, "nv", axis=0).codes.view(cols, 16))
+
+
 def test_refusals():
     X = torch.zeros((4, 32), device="cuda")
     w, m = torch.ones(32, device="cuda"), torch.zeros(4, device="cuda")
@@ -279,6 +361,7 @@ def test_refusals():
                  lambda: api.layer_norm_fwd(X, save="int8"), lambda: api.layer_norm_fwd(X, out=X[:3]),
                  lambda: api.layer_norm_fwd(X, torch.ones(64, device="cuda")[::2]),
                  lambda: api.layer_norm_fwd(X[None]),
+                 lambda: api.layer_norm_fwd(X.view(2, 64)[:, :32], out=X.view(-1)[:64].view(2, 32)),
                  lambda: api.layer_norm_bwd(X, X[:3], m, m), lambda: api.layer_norm_bwd(X, a, m, m),
                  lambda: api.layer_norm_bwd(X, X, m[:3], m),
                  lambda: api.layer_norm_bwd(X, X, m, m, want_dx=False, want_dw=False, want_db=False)):
