@@ -65,13 +65,6 @@ struct NormCols {
   MDEV bool whole(int i) const {
     return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? col(i) >= lo && col(i) + E <= hi : col(i) + E <= hi);
   }
-  // every unit of the warp (by whole warps)
-  MDEV bool all_whole() const {
-    bool w = true;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) w = w && whole(i);
-    return __all_sync(0xFFFFFFFFu, w);
-  }
   MDEV bool has(int i, int j) const { return col(i) + j < hi && (MODE != kPhase || col(i) + j >= lo); }
 };
 
@@ -117,9 +110,40 @@ MDEV void load_vector(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, const void* 
   }
 }
 
-// Unit i of an output row of type TY at `p` (its first column's place); kWhole: the
-// unit is known to be whole.
-template <bool kWhole, typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
+// kPhase with 32 lanes a row: the elements of a row's first and last unit that are
+// partly outside it.  Lanes 0 to E - 1 of the warp that holds the first unit have
+// one element of it each, lanes 16 to 16 + E - 1 of the one that holds the last; the
+// units themselves read zero.  So a ragged end costs a lane one element a row, and
+// no lane a mask.  (Rows of several to a warp are masked element by element.)
+template <int SPAN, int MODE>
+constexpr bool norm_edges = MODE == kPhase && SPAN == 32;
+
+struct NormEdge {
+  bool on;            // this lane has an element
+  bool first, last;   // the warp has a part of a unit at the row's begin, at its end
+  int first_owner, last_owner, last_unit;   // the lanes that hold them, and the last one's index there
+  int unit, owner;    // this lane's element's unit and its lane,
+  int elem, col;      // its place in the unit, and its column
+  template <int SPAN, int NV, int E, int MODE, int SHAPE>
+  MDEV explicit NormEdge(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs) {
+    // (rows of 32 lanes are longer than two units: none holds both ends)
+    const int lane = threadIdx.x & 31, begin = cs.c0 - lane * E, end = cs.hi - begin;
+    first = begin < 0 && -begin % E != 0;
+    first_owner = max(-begin, 0) / E;
+    last = end > 0 && end < SPAN * NV * E && end % E != 0;
+    last_unit = end / (SPAN * E);
+    last_owner = end / E % SPAN;
+    const bool tail = lane >= 16;
+    elem = lane & 15;
+    unit = tail ? last_unit : 0;
+    owner = tail ? last_owner : first_owner;
+    col = begin + (unit * SPAN + owner) * E + elem;
+    on = (tail ? last : first) && elem < E && col >= cs.lo && col < cs.hi;
+  }
+};
+
+// Unit i of an output row of type TY at `p` (its first column's place).
+template <typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
 MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, const float* v, int i, bool active) {
   if constexpr (MODE == kAny) {
     Unit<TY> u;
@@ -128,9 +152,9 @@ MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, co
   } else {
     Unit<TY, E> u;
     u.put(v);
-    if (active && (kWhole || cs.whole(i))) {
+    if (active && cs.whole(i)) {
       u.store(p);
-    } else if (MODE == kPhase && !kWhole && active && cs.some(i)) {
+    } else if (MODE == kPhase && !norm_edges<SPAN, MODE> && active && cs.some(i)) {
 #pragma unroll
       for (int j = 0; j < E; ++j)
         if (cs.has(i, j)) p[j] = u.elem(j);
@@ -139,13 +163,13 @@ MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, co
 }
 
 // y: the row's place of column 0.
-template <bool kWhole, int SPAN, int NV, int E, int MODE, int SHAPE>
+template <int SPAN, int NV, int E, int MODE, int SHAPE>
 MDEV void store_row_unit_any(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, void* y, int dtype, const float* v, int i,
                              bool active) {
   if (dtype == METIS_BF16)
-    store_row_unit<kWhole>(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
+    store_row_unit(cs, static_cast<__nv_bfloat16*>(y) + cs.col(i), v, i, active);
   else
-    store_row_unit<kWhole>(cs, static_cast<float*>(y) + cs.col(i), v, i, active);
+    store_row_unit(cs, static_cast<float*>(y) + cs.col(i), v, i, active);
 }
 
 // s / n for n's rounded reciprocal: one correction of the product (Markstein),

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
   using XS = UnitSlot<DX, E, MODE, 32, SPAN>;      // dense x
   using Ex = Exchange<2, SHAPE>;
   constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kMulti = Cols::kMulti, CL = Cols::kClustered;
+  constexpr bool kEdges = norm_edges<SPAN, MODE>;
   constexpr int kSpan = SPAN, kMost = Ex::kMost, kOwn = NV * E, kStage = Stage::kBytes;
   static_assert(kDense || MODE != kPhase, "the 8-bit blocks are columns of the matrix: no shift");
   extern __shared__ __align__(16) uint8_t ring[];
@@ -167,10 +168,9 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
   load_vector(cs, p.w, p.w_dtype, 1.f, w);
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) aw[k] = ab[k] = 0.f;
-  // a second body for warps without a partial unit: 65536 x 1001 takes 130 us with it
-  // against 150; rows of several warps have no registers for it
-  constexpr bool kEasy = MODE == kPhase && !kMulti;
-  const bool easy = kEasy && cs.all_whole();
+  const NormEdge edge(cs);
+  const float we = kEdges && edge.on && p.w ? load_any(p.w, p.w_dtype, edge.col) : 1.f;
+  float awe = 0.f, abe = 0.f;             // dw and db of that element's column
   if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
   uint32_t from = ring0;
   // all threads of a row leave the loop together; with several rows in a warp,
@@ -186,17 +186,17 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     }
     fetch_stats(row + cs.step);
     cp_async_wait<S - 1>();
-    auto g_unit = [&](int i, bool whole) {
+    auto g_unit = [&](int i) {
       const uint32_t at = from + i * Stage::kOne;
       if constexpr (MODE == kAny) {
         return GS::finish(at, lane, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
         Unit<TG, E> u = GS::finish(at, lane);
-        if (MODE == kPhase && !whole && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+        if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
         return u;
       }
     };
-    auto x_unit = [&](int i, bool whole) {
+    auto x_unit = [&](int i) {
       const uint32_t at = from + i * Stage::kOne + GS::kBytes;
       XUnit<TX, E> x;
       if constexpr (!kDense) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
         x.u = XS::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
       } else {
         x.u = XS::finish(at, lane);
-        if (MODE == kPhase && !whole && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
+        if (MODE == kPhase && !kEdges && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
       }
       return x;
     };
@@ -216,33 +216,50 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     XUnit<TX, E> xu[kKeep ? NV : 1];
     Unit<TG, E> gu[kKeep ? NV : 1];
     float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
-    auto sums = [&](auto whole) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float xh[E], dy[E];
-        const XUnit<TX, E> xv = x_unit(i, decltype(whole)::value);
-        const Unit<TG, E> gv = g_unit(i, decltype(whole)::value);
-        if constexpr (kKeep) {
-          xu[i] = xv;
-          gu[i] = gv;
-        }
-        xv.normed(p.saved.fmt, mean, rstd, xh);
-        gv.get(dy);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int k = E * i + j;
-          const float gk = dy[j] * w[k];
-          s1 = fmaf(gk, xh[j], s1);
-          s2 += gk;
-          aw[k] = fmaf(dy[j], xh[j], aw[k]);
-          ab[k] += dy[j];
-        }
+    float xe = 0.f, ge = 0.f;               // this lane's element of the row's ends: x - mean, and dy
+    if constexpr (kEdges) {
+      __syncwarp();                         // other lanes copied it
+      if (edge.on) {
+        const uint32_t at = from + edge.unit * Stage::kOne;
+        ge = GS::elem(at, edge.owner, edge.elem);
+        xe = XS::elem(at + GS::kBytes, edge.owner, edge.elem) - mean;
       }
-    };
-    if (kEasy && easy)
-      sums(std::true_type{});
-    else
-      sums(std::false_type{});
+      __syncwarp();
+      if (edge.first && lane == edge.first_owner) {
+        GS::clear(from, lane);
+        XS::clear(from + GS::kBytes, lane);
+      }
+      if (edge.last && lane == edge.last_owner) {
+        GS::clear(from + edge.last_unit * Stage::kOne, lane);
+        XS::clear(from + edge.last_unit * Stage::kOne + GS::kBytes, lane);
+      }
+      const float xh = xe * rstd, gk = ge * we;
+      s1 = gk * xh;
+      s2 = gk;
+      awe = fmaf(ge, xh, awe);
+      abe += ge;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float xh[E], dy[E];
+      const XUnit<TX, E> xv = x_unit(i);
+      const Unit<TG, E> gv = g_unit(i);
+      if constexpr (kKeep) {
+        xu[i] = xv;
+        gu[i] = gv;
+      }
+      xv.normed(p.saved.fmt, mean, rstd, xh);
+      gv.get(dy);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int k = E * i + j;
+        const float gk = dy[j] * w[k];
+        s1 = fmaf(gk, xh[j], s1);
+        s2 += gk;
+        aw[k] = fmaf(dy[j], xh[j], aw[k]);
+        ab[k] += dy[j];
+      }
+    }
     if (p.dX) {
       float c1, c2;
       if constexpr (!kMulti) {
@@ -270,26 +287,23 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
       // dx = rstd g + (x - mean) kd + k0
       const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -rstd * (c2 * p.inv_n);
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
-      auto put = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float x[E], dy[E];
-          if constexpr (kKeep) {
-            xu[i].affine(p.saved.fmt, mean, kd, k0, x);
-            gu[i].get(dy);
-          } else {
-            x_unit(i, decltype(whole)::value).affine(p.saved.fmt, mean, kd, k0, x);
-            g_unit(i, decltype(whole)::value).get(dy);
-          }
-#pragma unroll
-          for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
-          store_row_unit_any<decltype(whole)::value>(cs, out, p.dx_dtype, dy, i, active);
+      for (int i = 0; i < NV; ++i) {
+        float x[E], dy[E];
+        if constexpr (kKeep) {
+          xu[i].affine(p.saved.fmt, mean, kd, k0, x);
+          gu[i].get(dy);
+        } else {
+          x_unit(i).affine(p.saved.fmt, mean, kd, k0, x);
+          g_unit(i).get(dy);
         }
-      };
-      if (kEasy && easy)
-        put(std::true_type{});
-      else
-        put(std::false_type{});
+#pragma unroll
+        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
+        store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
+      }
+      if constexpr (kEdges) {
+        if (edge.on) store_any(out, p.dx_dtype, edge.col, fmaf(ge * we, rstd, fmaf(xe, kd, k0)));
+      }
     }
     from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
@@ -309,7 +323,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          if (cs.has(i, j)) gather[(tid / SPAN) * (SPAN * kOwn) + cs.col(i) + j] = a[E * i + j];
+          if (kEdges ? cs.whole(i) : cs.has(i, j)) gather[(tid / SPAN) * (SPAN * kOwn) + cs.col(i) + j] = a[E * i + j];
+      if (kEdges && edge.on) gather[(tid / SPAN) * (SPAN * kOwn) + edge.col] = which == 0 ? awe : abe;
       __syncthreads();
       for (int c = tid; c < p.cols; c += kLaneThreads) {
         float s = 0.f;
@@ -329,9 +344,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
         } else {
 #pragma unroll
           for (int j = 0; j < E; ++j)
-            if (cs.has(i, j)) part[cs.col(i) + j] = a[E * i + j];
+            if (kEdges ? cs.whole(i) : cs.has(i, j)) part[cs.col(i) + j] = a[E * i + j];
         }
       }
+      if (kEdges && edge.on) part[edge.col] = which == 0 ? awe : abe;
     }
   }
 }

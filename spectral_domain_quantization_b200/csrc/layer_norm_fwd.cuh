@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Slot = UnitSlot<T, E, MODE, 32, SPAN>;
   constexpr bool kRest = sizeof(T) == 4, CL = Cols::kClustered, kMulti = Cols::kMulti;
+  constexpr bool kEdges = norm_edges<SPAN, MODE>;
   constexpr int kSpan = SPAN, kStage = NV * Slot::kBytes;
   using Ex = Exchange<kRest ? 3 : 2, SHAPE>;
   constexpr int kMost = Ex::kMost;
@@ -93,7 +94,9 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
   const float lane_n = kMulti && lane < ex.warps ? columns_of(lane) : 0.f;
   const float inv_lane = lane_n > 0.f ? __fdiv_rn(1.f, lane_n) : 0.f;
   const float n_0 = columns_of(0), inv_0 = __fdiv_rn(1.f, n_0);
-  const bool easy = MODE == kPhase && cs.all_whole();
+  const NormEdge edge(cs);
+  const float we = kEdges && edge.on && p.w ? load_any(p.w, p.w_dtype, edge.col) : 1.f;
+  const float be = kEdges && edge.on && p.b ? load_any(p.b, p.w_dtype, edge.col) : 0.f;
   float top = 0.f;
   if constexpr (CL) cluster_sync_all();   // every CTA of the cluster runs before its shared memory is written
   uint32_t from = ring0;
@@ -105,48 +108,55 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
     cp_async_wait<S - 1>();
     float v[NV * E], part[NV];
     Unit<T, E> kept[MODE == kAny && SAVE ? NV : 1];
-float sum, m, p2[NV], p1[NV];
-    auto sums = [&](auto easy) {
-      constexpr bool kEasy = decltype(easy)::value;   // every unit of the warp is whole
+    float xe = 0.f;                         // this lane's element of the row's ends
+    if constexpr (kEdges) {
+      __syncwarp();                         // other lanes copied it
+      if (edge.on) xe = Slot::elem(from + edge.unit * Slot::kBytes, edge.owner, edge.elem);
+      __syncwarp();
+      if (edge.first && lane == edge.first_owner) Slot::clear(from, lane);
+      if (edge.last && lane == edge.last_owner) Slot::clear(from + edge.last_unit * Slot::kBytes, lane);
+    }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t at = from + i * Slot::kBytes;
-        Unit<T, E> u;
-        if constexpr (MODE == kAny) {
-          u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
-          if constexpr (SAVE) kept[i] = u;
-        } else {
-          u = Slot::finish(at, lane);
-          if (MODE == kPhase && !kEasy && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
-        }
-        u.get(v + E * i);
-        part[i] = tree_sum<E>(v + E * i);
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t at = from + i * Slot::kBytes;
+      Unit<T, E> u;
+      if constexpr (MODE == kAny) {
+        u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
+        if constexpr (SAVE) kept[i] = u;
+      } else {
+        u = Slot::finish(at, lane);
+        if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
       }
-      sum = span_sum<kSpan>(tree_sum_any<NV>(part));
-      m = divide(sum, n_w, inv_w);
+      u.get(v + E * i);
+      part[i] = tree_sum<E>(v + E * i);
+    }
+    if constexpr (kEdges) part[0] += xe;
+    const float sum = span_sum<kSpan>(tree_sum_any<NV>(part));
+    const float m = divide(sum, n_w, inv_w);
+    float p2[NV], p1[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float e[E];
+    for (int i = 0; i < NV; ++i) {
+      float e[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
-        if (MODE != kAligned && !kEasy && !cs.whole(i)) {
+      for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
+      if (MODE != kAligned && !kEdges && !cs.whole(i)) {
 #pragma unroll
-          for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
-        }
+        for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
+      }
+      p2[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
+      if constexpr (kRest) p1[i] = tree_sum<E>(e);
+      if ((MODE == kAligned || kEdges) && !cs.whole(i)) {
         p2[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
-        if constexpr (kRest) p1[i] = tree_sum<E>(e);
-        if (MODE == kAligned && !cs.whole(i)) {
-          p2[i] = 0.f;
-          if constexpr (kRest) p1[i] = 0.f;
-        }
+        if constexpr (kRest) p1[i] = 0.f;
       }
-    };
-    if (MODE == kPhase && easy)
-      sums(std::true_type{});
-    else
-      sums(std::false_type{});
+    }
+    if constexpr (kEdges) {
+      const float e = edge.on ? xe - m : 0.f;
+      p2[0] = fmaf(e, e, p2[0]);
+      if constexpr (kRest) p1[0] += e;
+    }
     float sq = tree_sum_any<NV>(p2), rest = 0.f;
     if constexpr (kRest) rest = tree_sum_any<NV>(p1);
     RowStats st;
@@ -212,22 +222,19 @@ float sum, m, p2[NV], p1[NV];
       if (p.rstd) p.rstd[row] = st.rstd;
     }
     void* y = static_cast<char*>(p.Y) + row * p.ldy * (p.y_dtype == METIS_BF16 ? 2 : 4);
-    auto put = [&](auto easy) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float o[E];
+    for (int i = 0; i < NV; ++i) {
+      float o[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int k = E * i + j;
-          o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
-        }
-        store_row_unit_any<decltype(easy)::value>(cs, y, p.y_dtype, o, i, active);
+      for (int j = 0; j < E; ++j) {
+        const int k = E * i + j;
+        o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
       }
-    };
-    if (MODE == kPhase && easy)
-      put(std::true_type{});
-    else
-      put(std::false_type{});
+      store_row_unit_any(cs, y, p.y_dtype, o, i, active);
+    }
+    if constexpr (kEdges) {
+      if (edge.on) store_any(y, p.y_dtype, edge.col, fmaf(fmaf(xe - st.m0, st.rstd, st.off), we, be));
+    }
     if constexpr (SAVE) {
       float x[NV][E];
       uint32_t codes[NV][E / 4];

@@ -362,6 +362,24 @@ struct UnitSlot {
     lds<Unit<T, E>::kWords>(base + kWord * tid, u.w);
     return u;
   }
+  // element j of thread tid's unit, and zeros in the place of the unit
+  static MDEV float elem(uint32_t base, int tid, int j) {
+    const uint32_t a = base + kWord * tid + static_cast<uint32_t>(sizeof(T)) * j;
+    if constexpr (sizeof(T) == 2) {
+      uint16_t h;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+      return __bfloat162float(__ushort_as_bfloat16(h));
+    } else {
+      float f;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+      return f;
+    }
+  }
+  static MDEV void clear(uint32_t base, int tid) {
+#pragma unroll
+    for (int i = 0; i < kWord / 8; ++i)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(base + kWord * tid + 8 * i), "r"(0u) : "memory");
+  }
 };
 
 // kAny: the aligned chunks that the unit lies in, and one more for the last of
