@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
   cp_async_wait<0>();
+  asm volatile("griddepcontrol.launch_dependents;");   // the kernel that adds the partial sums waits for this one's end
   // this CTA's partial sums; the ring's memory is free
   float* gather = reinterpret_cast<float*>(ring);
   const int64_t blk = CL ? blockIdx.x / ctas : blockIdx.x;
