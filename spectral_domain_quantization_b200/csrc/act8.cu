@@ -8,6 +8,7 @@
 #include "abi_common.h"
 #include "act8.cuh"
 #include "act8.h"
+#include "dependent.cuh"
 #include "fp4_block.cuh"
 #include "rows.cuh"
 
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kThreads) act8_save_kernel(const T* X, int64_t
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   const Span span = span_of<T>(X, rows, cols, ld);
   float top = 0.f;
+  wait_for_previous();
   // the loop's bound is the same for a warp
   for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
        u0 += kU * stride) {
@@ -134,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View in, int
   constexpr int kU = 32 / E;
   const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  wait_for_previous();
   for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 - lane < map.total;
        u0 += kU * stride) {
     uint32_t raw[kU][E / 4];
@@ -218,8 +221,8 @@ void save_shape(const T* X, int64_t rows, int64_t cols, int64_t ld, const Act8Vi
   const UnitMap map = unit_map(rows, 4 * out.blocks);
   auto* kernel = act8_save_kernel<FMT, T, SHAPE>;
   static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
-  kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(X, rows, cols, ld, out,
-                                                                                             map);
+  const int grid = grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms);
+  launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, s, X, rows, cols, ld, out, map);
 }
 
 template <int FMT, typename T, int SHAPE>
@@ -228,7 +231,8 @@ void restore_shape(const Act8View& in, int64_t rows, int64_t cols, T* Y, int64_t
   const UnitMap map = unit_map(rows, (cols + E - 1) / E);
   auto* kernel = act8_restore_kernel<FMT, T, SHAPE>;
   static const int per_sm = occupancy(reinterpret_cast<const void*>(kernel));
-  kernel<<<grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms), kThreads, 0, s>>>(in, cols, Y, ld, map);
+  const int grid = grid_for(per_sm, (map.total + kThreads - 1) / kThreads, num_sms);
+  launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, s, in, cols, Y, ld, map);
 }
 
 template <int FMT, typename T>
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
   __shared__ __align__(16) uint8_t sc_tile[128 * kNb];
   __shared__ __align__(16) uint8_t code_tile[AXIS == 0 ? 128 * kLdc : 16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  wait_for_previous();
   float s_t = 1.f;
   if (FMT4 == METIS_NVFP4) {
     float m = 0.f;
@@ -519,7 +524,7 @@ void quantize_axis(const Act8QuantParams& params, int num_sms, cudaStream_t s) {
   const int grid = grid_for(per_sm, static_cast<int64_t>(p.otiles) * p.itiles, num_sms);
   p.step_o = grid / p.itiles;
   p.step_i = grid % p.itiles;
-  kernel<<<grid, kThreads, kSmem, s>>>(p);
+  launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, kSmem, 1, s, p);
 }
 
 template <int FMT8, int FMT4>

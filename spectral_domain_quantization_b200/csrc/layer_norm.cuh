@@ -15,14 +15,16 @@
 #include <type_traits>
 
 #include "act8.cuh"
+#include "dependent.cuh"
 #include "layer_norm.h"
 #include "rows.cuh"
 
 namespace metis {
 
 // How a kernel spreads rows: kLanes, the SPAN lanes of a warp hold a row, and a
-// CTA of 128 threads takes 128 / SPAN of them; kCta, a CTA holds a row; kCluster.
-enum NormShape { kLanes = 0, kCta = 1, kCluster = 2 };
+// CTA of 128 threads takes 128 / SPAN of them; kCta, a CTA holds a row; kCluster;
+// kTall, a CTA that fills an SM holds a row (backward).
+enum NormShape { kLanes = 0, kCta = 1, kCluster = 2, kTall = 3 };
 
 constexpr int kLaneThreads = 128;
 constexpr int kWarpCols = 1024;        // columns of a warp of kCta and kCluster
@@ -281,23 +283,6 @@ inline int64_t norm_blocks(int64_t blocks, int rows, int period) {
   int64_t unit = 1;
   while ((unit * rows) % period) ++unit;
   return imax64(unit, blocks / unit * unit);
-}
-
-// Launch `kernel` on `grid` CTAs, in clusters of `ctas` where that is not 1.
-template <typename P>
-void norm_launch(void (*kernel)(P, int), int grid, int threads, int smem, int ctas, const P& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, kernel, p, ctas);
 }
 
 // What is known of a kernel: the CTAs of W warps that an SM holds, and on which

@@ -7,14 +7,13 @@ namespace metis {
 namespace {
 
 // out[c] = sum over the parts; 32 columns x 16 slices of the parts a CTA,
-// blockIdx.y picks dweight or dbias.  Launched while the kernel before it ends
-// (programmatic dependent launch), and waits for that kernel's writes.
+// blockIdx.y picks dweight or dbias.
 __global__ void __launch_bounds__(512) norm_reduce_kernel(const float* part_w, const float* part_b, int parts,
                                                           int64_t part_ld, int cols, float* dw, float* db) {
   __shared__ float acc[16][33];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   if (!out) return;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + x;
@@ -115,16 +114,8 @@ void launch_norm_bwd(const NormBwdParams& p, int parts, cudaStream_t s) {
 
 void launch_norm_reduce(const float* part_w, const float* part_b, int parts, int64_t part_ld, int cols, float* dw,
                         float* db, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32), 2);
-  cfg.blockDim = dim3(512);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, norm_reduce_kernel, part_w, part_b, parts, part_ld, cols, dw, db);
+  launch_dependent(norm_reduce_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, 1, s, part_w, part_b,
+                   parts, part_ld, cols, dw, db);
 }
 
 }  // namespace metis

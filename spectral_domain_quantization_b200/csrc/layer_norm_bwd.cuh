@@ -93,9 +93,10 @@ struct BwdStage {
 };
 
 constexpr int kBwdWarps = 8;       // of a CTA
+constexpr int kTallWarps = 16;
 
 template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, int SHAPE>
-__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd_kernel(NormBwdParams p, int ctas) {
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256)) norm_bwd_kernel(NormBwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
   using GS = UnitSlot<TG, E, MODE, 32, SPAN>;
@@ -161,11 +162,35 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
         next_sc[i] = on && cs.left(i) > 0 ? p.saved.scales[row * p.saved.blocks + (cs.col(i) >> 5)] : 0u;
     }
   };
+  wait_for_previous();
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch();
   fetch_stats(cs.row);
   float w[kOwn], aw[kOwn], ab[kOwn];
   load_vector(cs, p.w, p.w_dtype, 1.f, w);
+  // kTall: 128 registers a thread have no room for the weights; each thread keeps
+  // its own behind the ring
+  constexpr bool kStaged = SHAPE == kTall;
+  const uint32_t w_at = smem_u32(ring) + (blockDim.x >> 5) * (S * kStage) + 16 * tid;
+  if constexpr (kStaged) {
+#pragma unroll
+    for (int k = 0; k < kOwn / 4; ++k)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * k * blockDim.x), "f"(w[4 * k]),
+                   "f"(w[4 * k + 1]), "f"(w[4 * k + 2]), "f"(w[4 * k + 3])
+                   : "memory");
+  }
+  auto w_unit = [&](int i, float* o) {
+    if constexpr (kStaged) {
+      uint32_t u[E];
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) lds16(w_at + 16 * (i * (E / 4) + k) * blockDim.x, u + 4 * k);
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] = __uint_as_float(u[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] = w[E * i + j];
+    }
+  };
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) aw[k] = ab[k] = 0.f;
   const NormEdge edge(cs);
@@ -241,7 +266,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float xh[E], dy[E];
+      float xh[E], dy[E], wu[E];
+      w_unit(i, wu);
       const XUnit<TX, E> xv = x_unit(i);
       const Unit<TG, E> gv = g_unit(i);
       if constexpr (kKeep) {
@@ -253,7 +279,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int k = E * i + j;
-        const float gk = dy[j] * w[k];
+        const float gk = dy[j] * wu[j];
         s1 = fmaf(gk, xh[j], s1);
         s2 += gk;
         aw[k] = fmaf(dy[j], xh[j], aw[k]);
@@ -289,7 +315,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float x[E], dy[E];
+        float x[E], dy[E], wu[E];
+        w_unit(i, wu);
         if constexpr (kKeep) {
           xu[i].affine(p.saved.fmt, mean, kd, k0, x);
           gu[i].get(dy);
@@ -298,7 +325,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
           g_unit(i).get(dy);
         }
 #pragma unroll
-        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * w[E * i + j], rstd, x[j]);
+        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * wu[j], rstd, x[j]);
         store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
       }
       if constexpr (kEdges) {
@@ -308,7 +335,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 256) norm_bwd
     from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
   cp_async_wait<0>();
-  asm volatile("griddepcontrol.launch_dependents;");   // the kernel that adds the partial sums waits for this one's end
+  launch_next();   // the kernel that adds the partial sums waits for this one's end
   // this CTA's partial sums; the ring's memory is free
   float* gather = reinterpret_cast<float*>(ring);
   const int64_t blk = CL ? blockIdx.x / ctas : blockIdx.x;
@@ -362,20 +389,22 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
   // two stages and the CTAs that then fit an SM: three stages take 84.2 us against
   // 82.8 on 16384 x 4096 bf16, and 150.8 against 129.6 in float32
   constexpr int S = 2;
-  constexpr int kWarp = S * kStage > kGather ? S * kStage : kGather;
+  constexpr int kStaged = SHAPE == kTall ? 4 * kWarpCols : 0, kMostWarps = SHAPE == kTall ? kTallWarps : kBwdWarps;
+  constexpr int kWarp = (S * kStage > kGather ? S * kStage : kGather) + kStaged;
   auto* kernel = norm_bwd_kernel<TX, TG, SPAN, NV, E, S, MODE, SHAPE>;
   static NormHeld held;
   NormBwdParams p = params;
-  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), kBwdWarps);
+  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), kMostWarps);
   p.slice = plan.slice;
   const int smem = plan.warps * kWarp;
-  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kBwdWarps) * kWarp);
+  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kMostWarps) * kWarp);
   if (occupancy) {
     const int64_t most = imax64(1, static_cast<int64_t>(num_sms) * per_sm / plan.ctas);
     return static_cast<int>(
         norm_blocks(imin64((p.rows + Cols::kRows - 1) / Cols::kRows, most), Cols::kRows, p.period));
   }
-  norm_launch(kernel, parts * plan.ctas, 32 * plan.warps, smem, plan.ctas, p, s);
+  launch_dependent(kernel, dim3(static_cast<unsigned>(parts * plan.ctas)), 32 * plan.warps, static_cast<size_t>(smem),
+                   plan.ctas, s, p, plan.ctas);
   return 0;
 }
 
@@ -395,6 +424,14 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
     if (cols <= 1280) return norm_bwd_go<TX, TG, 32, 40 / E, E, MODE, kLanes>(p, parts, occ, num_sms, s);
   }
   if (cols <= kBwdWarps * kWarpCols) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCta>(p, parts, occ, num_sms, s);
+  // A cluster's CTAs of more than 5 warps leave an SM room for one, and half its
+  // threads idle: from there one CTA of 16 warps has the row.  4000 rows of bf16:
+  // 12288 columns 80.5 us against 86.2 in a cluster, 14336 from 8 bits 98.4 against
+  // 123.8, 14335 118 against 157; 10240 columns 73.7 against 67.2.
+  if constexpr (E == 8 && MODE != kAny) {
+    if (cols > 10 * kWarpCols && cols <= kTallWarps * kWarpCols)
+      return norm_bwd_go<TX, TG, 32, NV, E, MODE, kTall>(p, parts, occ, num_sms, s);
+  }
   return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCluster>(p, parts, occ, num_sms, s);
 }
 

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
     fetch_row += cs.step;
     into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
   };
+  wait_for_previous();
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch();
   float w[NV * E], b[NV * E];
@@ -302,8 +303,8 @@ void norm_fwd_go(const NormFwdParams& params, int num_sms, cudaStream_t s) {
   const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kFwdWarps) * kWarp);
   const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX) / plan.ctas;
   const int64_t blocks = imin64((p.rows + Cols::kRows - 1) / Cols::kRows, imax64(1, most));
-  norm_launch(kernel, static_cast<int>(norm_blocks(blocks, Cols::kRows, p.period)) * plan.ctas, 32 * plan.warps, smem,
-              plan.ctas, p, s);
+  launch_dependent(kernel, dim3(static_cast<unsigned>(norm_blocks(blocks, Cols::kRows, p.period) * plan.ctas)),
+                   32 * plan.warps, static_cast<size_t>(smem), plan.ctas, s, p, plan.ctas);
 }
 
 // E columns a unit, 32 a thread (16 where a row has 64 or fewer; 40 or 48 where that
