@@ -326,6 +326,74 @@ def test_two_threads_on_one_stream():
             assert torch.equal(dw, want[k][1]) and torch.equal(db, want[k][2])
 
 
+@pytest.mark.parametrize("cols", [515, 769, 1021, 1026, 1275, 1277, 1531, 2041, 2049, 10243, 16373, 16381])
+@pytest.mark.parametrize("dtype,gdtype", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_every_begin(cols, dtype, gdtype):
+    # rows that begin and end at every place of a 16-byte word, and of two
+    for offset in (range(8) if cols < 2000 else (1, 6)):
+        x, dy, w, b = data(9, cols, seed=offset)
+        X, dY, w, b = mat(x, dtype, 0, offset), mat(dy, gdtype, 0, offset), w.cuda(), b.cuda()
+        r = api.layer_norm_fwd(X, w, b)
+        check_fwd(r, X, w, b)
+        check_bwd(api.layer_norm_bwd(dY, X, r.mean, r.rstd, w), dY, np64(X), r.mean, r.rstd, w)
+
+
+@pytest.mark.parametrize("cols", [1100, 1272, 1280, 10240, 10248, 11000, 12288, 16384])
+@pytest.mark.parametrize("kind", ["bf16", "mxint8", "mxfp8"])
+def test_backward_of_few_long_rows(cols, kind):
+    for rows in (1, 3, 200):
+        x, dy, w, _ = data(rows, cols, seed=30)
+        X, dY, w = mat(x, "bf16"), mat(dy, "bf16"), w.cuda()
+        r = api.layer_norm_fwd(X, w, save=None if kind == "bf16" else kind)
+        given = X if r.saved is None else r.saved
+        x64 = np64(X) if r.saved is None else act8_ref.load(*act8_ref.save(np64(X), kind), cols, kind)
+        for weight in (w, None):
+            check_bwd(api.layer_norm_bwd(dY, given, r.mean, r.rstd, weight), dY, x64, r.mean, r.rstd, weight)
+
+
+def test_between_other_work():
+    # the launches overlap the end of what runs before them: copies, fills and
+    # library kernels that write their inputs, on one stream, over a fork and a
+    # join, eagerly and captured
+    x, dy, w, _ = data(2016, 1000, seed=40)
+    X0, dY0, w = mat(x, "bf16"), mat(dy, "bf16"), w.cuda()
+    X, dY = torch.zeros_like(X0), torch.zeros_like(dY0)
+    side = torch.cuda.Stream()
+
+    def step():
+        X.copy_(X0)
+        r = api.layer_norm_fwd(X, w, save="mxint8")
+        X.fill_(7)                                 # behind the forward's reads
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            back = api.restore_act8(r.saved)
+            kept = api.save_act8(back, "mxfp8")
+        dY.zero_()
+        dY.copy_(dY0)
+        d = api.layer_norm_bwd(dY, r.saved, r.mean, r.rstd, w)
+        dY.fill_(3)
+        torch.cuda.current_stream().wait_stream(side)
+        q = api.quantize_fp4_act8(kept, "nv", axis=0)
+        return [r.Y, r.mean, r.rstd, back, kept.codes, q.codes, q.scales] + list(d)
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    check_bwd(want[-3:], dY0, act8_ref.load(*act8_ref.save(np64(X0), "mxint8"), 1000, "mxint8"), want[1], want[2], w)
+    for _ in range(20):
+        got = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(20):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_offsets_past_32_bits():
     # 2.3e9 elements: the rows at the end against the same rows alone
     rows, cols, tail = 70000, 32768, 40
