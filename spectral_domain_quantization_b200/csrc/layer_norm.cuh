@@ -45,6 +45,7 @@ struct NormCols {
   int t;              // lane of the row's lanes in the warp
   bool first, last;   // it is the first, the last of them
   int64_t row, step;  // first row, and from one to the next
+  uint32_t all, any;  // kPhase: bit i, all or any of unit i's columns are the row's
 
   // kPhase: row r's first element is (offset + r ld) mod `width` elements behind a
   // period's begin; that of rows `period` apart is equal
@@ -60,15 +61,30 @@ struct NormCols {
     c0 = begin + t * E + (kMulti ? static_cast<int>(threadIdx.x >> 5) * kWarpCols : 0);
     lo = max(begin, 0);
     hi = kClustered ? min(cols, begin + slice) : cols;
+    all = any = 0u;
+    if (MODE == kPhase) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (col(i) >= lo && col(i) + E <= hi) all |= 1u << i;
+        if (col(i) < hi && col(i) + E > lo) any |= 1u << i;
+      }
+    }
   }
   MDEV int col(int i) const { return c0 + i * kStride; }
   MDEV int left(int i) const { return hi - col(i); }      // columns from unit i's first on
-  MDEV bool some(int i) const { return MODE == kPhase ? col(i) < hi && col(i) + E > lo : col(i) < hi; }
+  MDEV bool some(int i) const { return MODE == kPhase ? (any >> i) & 1u : col(i) < hi; }
   MDEV bool whole(int i) const {
-    return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? col(i) >= lo && col(i) + E <= hi : col(i) + E <= hi);
+    return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? (all >> i) & 1u : col(i) + E <= hi);
   }
   MDEV bool has(int i, int j) const { return col(i) + j < hi && (MODE != kPhase || col(i) + j >= lo); }
 };
+
+// No aligned word that holds elements of the row at `x` reaches over the matrix.
+template <typename T>
+MDEV bool row_inside(const T* x, int cols, const Span& s) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x);
+  return a - 16 >= s.lo && a + cols * sizeof(T) + 16 <= s.hi;
+}
 
 // Per-column vector (weight or bias) into registers; `none` where it is absent.
 template <int SPAN, int NV, int E, int MODE, int SHAPE>

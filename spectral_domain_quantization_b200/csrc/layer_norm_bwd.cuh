@@ -121,25 +121,31 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // row `fetch_row` into the stage at `into`; what a row needs besides, its mean
   // and rstd and the scale codes of its 8-bit blocks, goes into registers one row
   // ahead
+  // (a second copy of the loads costs kCta's 16-byte units 40 registers a thread and
+  // so a CTA of the SM, 8192 x 4095 bf16 99 us against 74; rows of 40 columns a thread
+  // have no register left for it either)
+  constexpr bool kInside = MODE == kPhase && !(E == 8 && (SHAPE == kCta || NV > 4));
   int64_t fetch_row = cs.row;
   uint32_t into = ring0;
   auto fetch = [&] {
     const bool on = fetch_row < p.rows;
     if (SPAN < 32 || on) {
       const TG* g = dY + fetch_row * p.ldg;
+      const bool inside = kInside && on && row_inside(g, p.cols, gspan) &&
+                          (!kDense || row_inside(X + fetch_row * p.ldx, p.cols, xspan));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint32_t at = into + i * Stage::kOne;
         if constexpr (MODE == kAny)
           GS::start(at, lane, g + cs.col(i), on ? cs.left(i) : -16, cs.last, gspan);
         else
-          GS::start(at, lane, g + cs.col(i), on && cs.whole(i), on && cs.some(i), gspan);
+          GS::start(at, lane, g + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, gspan);
         if constexpr (kDense) {
           const DX* x = X + fetch_row * p.ldx;
           if constexpr (MODE == kAny)
             XS::start(at + GS::kBytes, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, xspan);
           else
-            XS::start(at + GS::kBytes, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), xspan);
+            XS::start(at + GS::kBytes, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, xspan);
         } else {
           cp_async<E>(at + GS::kBytes + E * lane, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
                       on && cs.left(i) > 0);

@@ -63,13 +63,14 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
     const bool on = fetch_row < p.rows;
     if (SPAN < 32 || on) {
       const T* x = X + fetch_row * p.ldx;
+      const bool inside = MODE == kPhase && on && row_inside(x, p.cols, span);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint32_t at = into + i * Slot::kBytes;
         if constexpr (MODE == kAny)
           Slot::start(at, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, span);
         else
-          Slot::start(at, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), span);
+          Slot::start(at, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, span);
       }
     }
     cp_async_commit();

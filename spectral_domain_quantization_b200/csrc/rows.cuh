@@ -334,10 +334,11 @@ template <typename T, int E, int MODE, int kThreads, int kSpan>
 struct UnitSlot {
   static constexpr int kWord = E * static_cast<int>(sizeof(T));
   static constexpr int kBytes = kWord * kThreads;
-  // `p`: the unit's first element; it has `whole` columns of the row, or `some`
-  static MDEV void start(uint32_t base, int tid, const T* p, bool whole, bool some, const Span& s) {
+  // `p`: the unit's first element; it has `whole` columns of the row, or `some`.
+  // `inside`: no word of the row reaches over the matrix
+  static MDEV void start(uint32_t base, int tid, const T* p, bool whole, bool some, bool inside, const Span& s) {
     const uint32_t dst = base + kWord * tid;
-    if constexpr (MODE == kAligned) {
+    if (MODE == kAligned || inside) {
       cp_async<kWord>(dst, p, some);
     } else {
       const uintptr_t a = reinterpret_cast<uintptr_t>(p);
