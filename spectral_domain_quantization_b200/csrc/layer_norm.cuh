@@ -23,7 +23,7 @@ namespace metis {
 
 // How a kernel spreads rows: kLanes, the SPAN lanes of a warp hold a row, and a
 // CTA of 128 threads takes 128 / SPAN of them; kCta, a CTA holds a row; kCluster;
-// kTall, a CTA that fills an SM holds a row (backward).
+// kTall, a CTA that fills an SM holds a row, for the widest that can.
 enum NormShape { kLanes = 0, kCta = 1, kCluster = 2, kTall = 3 };
 
 constexpr int kLaneThreads = 128;
@@ -43,7 +43,6 @@ struct NormCols {
   int c0;             // this thread's first column (kPhase: may be outside)
   int shift;          // kPhase: columns that c0 is moved by
   int t;              // lane of the row's lanes in the warp
-  bool first, last;   // it is the first, the last of them
   int64_t row, step;  // first row, and from one to the next
   uint32_t all, any;  // kPhase: bit i, all or any of unit i's columns are the row's
 
@@ -51,8 +50,6 @@ struct NormCols {
   // period's begin; that of rows `period` apart is equal
   MDEV NormCols(int cols, int slice, int ctas, int64_t ld, int offset, int width) {
     t = static_cast<int>(threadIdx.x) % SPAN;
-    first = t == 0;
-    last = t == SPAN - 1;
     const int64_t blocks = kClustered ? gridDim.x / ctas : gridDim.x;
     row = static_cast<int64_t>(kClustered ? blockIdx.x / ctas : blockIdx.x) * kRows + (kMulti ? 0 : threadIdx.x / SPAN);
     step = blocks * kRows;                // a multiple of the period
@@ -74,7 +71,7 @@ struct NormCols {
   MDEV int left(int i) const { return hi - col(i); }      // columns from unit i's first on
   MDEV bool some(int i) const { return MODE == kPhase ? (any >> i) & 1u : col(i) < hi; }
   MDEV bool whole(int i) const {
-    return MODE == kAligned ? col(i) < hi : (MODE == kPhase ? (all >> i) & 1u : col(i) + E <= hi);
+    return MODE == kPhase ? (all >> i) & 1u : col(i) < hi;
   }
   MDEV bool has(int i, int j) const { return col(i) + j < hi && (MODE != kPhase || col(i) + j >= lo); }
 };
@@ -94,38 +91,40 @@ MDEV void load_vector(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, const void* 
     for (int k = 0; k < NV * E; ++k) out[k] = none;
     return;
   }
-  if (MODE == kAligned && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+  if constexpr (MODE == kAligned) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = cs.some(i) ? cs.col(i) : 0;     // (the columns are a multiple of E)
-      if (dtype == METIS_BF16) {
-        Unit<__nv_bfloat16, E> u;
-        const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
+      for (int i = 0; i < NV; ++i) {
+        const int c = cs.some(i) ? cs.col(i) : 0;     // (the columns are a multiple of E)
+        if (dtype == METIS_BF16) {
+          Unit<__nv_bfloat16, E> u;
+          const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-          const uint2 x = q[k];
-          u.w[2 * k] = x.x;
-          u.w[2 * k + 1] = x.y;
-        }
-        u.get(out + E * i);
-      } else {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+          for (int k = 0; k < E / 4; ++k) {
+            const uint2 x = q[k];
+            u.w[2 * k] = x.x;
+            u.w[2 * k + 1] = x.y;
+          }
+          u.get(out + E * i);
+        } else {
+          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-          const float4 x = q[k];
-          out[E * i + 4 * k] = x.x;
-          out[E * i + 4 * k + 1] = x.y;
-          out[E * i + 4 * k + 2] = x.z;
-          out[E * i + 4 * k + 3] = x.w;
+          for (int k = 0; k < E / 4; ++k) {
+            const float4 x = q[k];
+            out[E * i + 4 * k] = x.x;
+            out[E * i + 4 * k + 1] = x.y;
+            out[E * i + 4 * k + 2] = x.z;
+            out[E * i + 4 * k + 3] = x.w;
+          }
         }
       }
+      return;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < E; ++j) out[E * i + j] = cs.has(i, j) ? load_any(p, dtype, cs.col(i) + j) : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < E; ++j) out[E * i + j] = cs.has(i, j) ? load_any(p, dtype, cs.col(i) + j) : 0.f;
 }
 
 // kPhase with 32 lanes a row: the elements of a row's first and last unit that are
@@ -164,9 +163,12 @@ struct NormEdge {
 template <typename TY, int SPAN, int NV, int E, int MODE, int SHAPE>
 MDEV void store_row_unit(const NormCols<SPAN, NV, E, MODE, SHAPE>& cs, TY* p, const float* v, int i, bool active) {
   if constexpr (MODE == kAny) {
-    Unit<TY> u;
-    u.put(v);
-    store_unit<TY, false>(p, u, active ? cs.left(i) : 0, cs.first, cs.last);
+    if (active && cs.whole(i)) {
+      if constexpr (sizeof(TY) == 2)
+        *p = __float2bfloat16_rn(*v);
+      else
+        *p = *v;
+    }
   } else {
     Unit<TY, E> u;
     u.put(v);

@@ -16,12 +16,12 @@ namespace metis {
 struct Act8Tag {};
 
 // Bytes of a unit of x in the ring, of a warp: dense, or E codes of the 8-bit copy.
-template <typename TX, int E, int MODE, int SPAN>
+template <typename TX, int E, int MODE>
 struct XBytes {
-  static constexpr int value = UnitSlot<TX, E, MODE, 32, SPAN>::kBytes;
+  static constexpr int value = UnitSlot<TX, E, MODE, 32>::kBytes;
 };
-template <int E, int MODE, int SPAN>
-struct XBytes<Act8Tag, E, MODE, SPAN> {
+template <int E, int MODE>
+struct XBytes<Act8Tag, E, MODE> {
   static constexpr int value = E * 32;
 };
 
@@ -87,9 +87,19 @@ struct DenseType<Act8Tag> {
 
 template <typename TX, typename TG, int SPAN, int NV, int E, int MODE>
 struct BwdStage {
-  static constexpr int kG = UnitSlot<TG, E, MODE, 32, SPAN>::kBytes;
-  static constexpr int kOne = kG + XBytes<TX, E, MODE, SPAN>::value;
+  static constexpr int kG = UnitSlot<TG, E, MODE, 32>::kBytes;
+  static constexpr int kOne = kG + XBytes<TX, E, MODE>::value;
   static constexpr int kBytes = NV * kOne;      // of a warp
+};
+template <typename TX, typename TG, int SPAN, int NV>
+struct BwdStage<TX, TG, SPAN, NV, 1, kAny> {
+  static constexpr int kG = RowImage<TG, SPAN, NV>::kBytes;
+  static constexpr int kOne = kG, kBytes = kG + RowImage<TX, SPAN, NV>::kBytes;
+};
+template <typename TG, int SPAN, int NV>
+struct BwdStage<Act8Tag, TG, SPAN, NV, 1, kAny> {
+  static constexpr int kG = RowImage<TG, SPAN, NV>::kBytes;
+  static constexpr int kOne = kG, kBytes = kG + 32 * NV;
 };
 
 constexpr int kBwdWarps = 8;       // of a CTA
@@ -99,9 +109,11 @@ template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, in
 __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256)) norm_bwd_kernel(NormBwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
-  using GS = UnitSlot<TG, E, MODE, 32, SPAN>;
+  using GS = UnitSlot<TG, E, MODE, 32>;
   using DX = typename DenseType<TX>::type;
-  using XS = UnitSlot<DX, E, MODE, 32, SPAN>;      // dense x
+  using XS = UnitSlot<DX, E, MODE, 32>;            // dense x
+  using GI = RowImage<TG, SPAN, NV>;               // kAny
+  using XI = RowImage<DX, SPAN, NV>;
   using Ex = Exchange<2, SHAPE>;
   constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kMulti = Cols::kMulti, CL = Cols::kClustered;
   constexpr bool kEdges = norm_edges<SPAN, MODE>;
@@ -117,6 +129,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   const Span gspan = span_of<TG>(p.dY, p.rows, p.cols, p.ldg);
   const Span xspan = span_of<DX>(p.X, p.rows, p.cols, p.ldx);
   const uint32_t ring0 = smem_u32(ring) + (tid >> 5) * (S * kStage);
+  // kAny, 8 bits: where a warp's elements wait as float32
+  const uint32_t d_at = smem_u32(ring) + (blockDim.x >> 5) * (S * kStage) + (tid >> 5) * (128 * NV);
 
   // row `fetch_row` into the stage at `into`; what a row needs besides, its mean
   // and rstd and the scale codes of its 8-bit blocks, goes into registers one row
@@ -133,22 +147,32 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
       const TG* g = dY + fetch_row * p.ldg;
       const bool inside = kInside && on && row_inside(g, p.cols, gspan) &&
                           (!kDense || row_inside(X + fetch_row * p.ldx, p.cols, xspan));
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t at = into + i * Stage::kOne;
-        if constexpr (MODE == kAny)
-          GS::start(at, lane, g + cs.col(i), on ? cs.left(i) : -16, cs.last, gspan);
-        else
-          GS::start(at, lane, g + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, gspan);
+      if constexpr (MODE == kAny) {
+        const int n = on ? cs.left(0) + cs.t : 0, c = cs.col(0) - cs.t;
+        GI::start(into, lane, g + c, n, gspan);
         if constexpr (kDense) {
-          const DX* x = X + fetch_row * p.ldx;
-          if constexpr (MODE == kAny)
-            XS::start(at + GS::kBytes, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, xspan);
-          else
-            XS::start(at + GS::kBytes, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, xspan);
+          XI::start(into + Stage::kG, lane, X + fetch_row * p.ldx + c, n, xspan);
         } else {
-          cp_async<E>(at + GS::kBytes + E * lane, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
-                      on && cs.left(i) > 0);
+          // SPAN * NV codes, 16 at a time (c is a multiple of 32, and the codes' rows
+          // are padded to one)
+          const uint8_t* q = p.saved.codes + fetch_row * p.saved.ldc + c;
+#pragma unroll
+          for (int k = 0; k < (NV + 15) / 16; ++k) {
+            const int at = 16 * (cs.t + SPAN * k);
+            if (at < SPAN * NV) cp_async16(into + Stage::kG + lane / SPAN * (SPAN * NV) + at, q + at, at < n ? 16 : 0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const uint32_t at = into + i * Stage::kOne;
+          GS::start(at, lane, g + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, gspan);
+          if constexpr (kDense)
+            XS::start(at + GS::kBytes, lane, X + fetch_row * p.ldx + cs.col(i), on && cs.whole(i), on && cs.some(i),
+                      inside, xspan);
+          else
+            cp_async<E>(at + GS::kBytes + E * lane, p.saved.codes + fetch_row * p.saved.ldc + cs.col(i),
+                        on && cs.left(i) > 0);
         }
       }
     }
@@ -157,12 +181,17 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
     into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
   };
   float next_mean = 0.f, next_rstd = 0.f;
-  uint32_t next_sc[kDense ? 1 : NV];
+  // kAny: lane t has the scale code of the t-th 8-bit block of its row's lanes
+  constexpr int kScales = kDense || MODE == kAny ? 1 : NV;
+  uint32_t next_sc[kScales];
   auto fetch_stats = [&](int64_t row) {
     const bool on = row < p.rows;
     next_mean = on ? p.mean[row] : 0.f;
     next_rstd = on ? p.rstd[row] : 0.f;
-    if constexpr (!kDense) {
+    if constexpr (!kDense && MODE == kAny) {
+      const int c = cs.col(0) - cs.t + 32 * cs.t;
+      next_sc[0] = on && 32 * cs.t < SPAN * NV && c < cs.hi ? p.saved.scales[row * p.saved.blocks + (c >> 5)] : 0u;
+    } else if constexpr (!kDense) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         next_sc[i] = on && cs.left(i) > 0 ? p.saved.scales[row * p.saved.blocks + (cs.col(i) >> 5)] : 0u;
@@ -207,45 +236,98 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // all threads of a row leave the loop together; with several rows in a warp,
   // all of the warp
   for (int64_t row = cs.row; SPAN == 32 ? row < p.rows : row - (lane / SPAN) < p.rows; row += cs.step) {
+    if constexpr (MODE == kAny) __syncwarp();      // every lane has read the stage that is copied to
     fetch();
     const bool active = SPAN == 32 || row < p.rows;
     const float mean = next_mean, rstd = next_rstd;
-    uint32_t sc[kDense ? 1 : NV];
-    if constexpr (!kDense) {
+    uint32_t sc[kScales];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sc[i] = next_sc[i];
-    }
+    for (int i = 0; i < kScales; ++i) sc[i] = kDense ? 0u : next_sc[i];
     fetch_stats(row + cs.step);
     cp_async_wait<S - 1>();
-    auto g_unit = [&](int i) {
-      const uint32_t at = from + i * Stage::kOne;
-      if constexpr (MODE == kAny) {
-        return GS::finish(at, lane, dY + row * p.ldg + cs.col(i), active ? cs.left(i) : 0, cs.last);
+    uint32_t g_at = 0u, x_at = 0u;
+    if constexpr (MODE == kAny) {
+      const int c = cs.col(0) - cs.t, n = cs.left(0) + cs.t;
+      __syncwarp();                         // other lanes copied it
+      GI::end(from, lane, dY + row * p.ldg + c, n);
+      if constexpr (kDense) XI::end(from + Stage::kG, lane, X + row * p.ldx + c, n);
+      __syncwarp();
+      g_at = GI::place(from, lane, dY + row * p.ldg + c);
+      if constexpr (kDense) {
+        x_at = XI::place(from + Stage::kG, lane, X + row * p.ldx + c);
       } else {
-        Unit<TG, E> u = GS::finish(at, lane);
+        // x - mean as float32 behind the ring, four codes of a block at a time
+        const uint32_t codes = from + Stage::kG + lane / SPAN * (SPAN * NV), wide = d_at + lane / SPAN * (4 * SPAN * NV);
+        const uint32_t factor = __float_as_uint(p.saved.fmt == METIS_MXINT8 ? act8_factor<METIS_MXINT8>(sc[0])
+                                                                            : act8_factor<METIS_MXFP8>(sc[0]));
+        auto decode = [&](auto fmt) {
+#pragma unroll
+          for (int j = 0; j < NV / 4; ++j) {
+            const int k = cs.t + SPAN * j;
+            const float f = __uint_as_float(__shfl_sync(0xFFFFFFFFu, factor, lane - cs.t + (k >> 3)));
+            uint32_t w;
+            lds<1>(codes + 4 * k, &w);
+            float v[4];
+            act8_elems4<decltype(fmt)::value>(w, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = fmaf(v[q], f, -mean);
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(wide + 16 * k), "f"(v[0]), "f"(v[1]),
+                         "f"(v[2]), "f"(v[3])
+                         : "memory");
+          }
+        };
+        if (p.saved.fmt == METIS_MXINT8)
+          decode(std::integral_constant<int, METIS_MXINT8>{});
+        else
+          decode(std::integral_constant<int, METIS_MXFP8>{});
+        __syncwarp();
+        x_at = wide + 4 * cs.t;
+      }
+    }
+    // dy of unit i, and (x - mean) a + b or (x - mean) rstd
+    auto g_unit = [&](int i, float* dy) {
+      if constexpr (MODE == kAny) {
+        *dy = GI::elem(g_at, i);
+      } else {
+        Unit<TG, E> u = GS::finish(from + i * Stage::kOne, lane);
         if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
-        return u;
+        u.get(dy);
+      }
+    };
+    auto centered = [&](int i) {
+      if constexpr (MODE != kAny) {
+        return 0.f;                         // (not called)
+      } else if constexpr (kDense) {
+        return XI::elem(x_at, i) - mean;
+      } else {
+        return lds_elem<float>(x_at + 4 * SPAN * i);
       }
     };
     auto x_unit = [&](int i) {
-      const uint32_t at = from + i * Stage::kOne + GS::kBytes;
-      XUnit<TX, E> x;
-      if constexpr (!kDense) {
-        lds<E / 4>(at + E * lane, x.w);
-        x.sc = sc[i];
-      } else if constexpr (MODE == kAny) {
-        x.u = XS::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
-      } else {
-        x.u = XS::finish(at, lane);
-        if (MODE == kPhase && !kEdges && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
+      XUnit<TX, MODE == kAny ? 4 : E> x;
+      if constexpr (MODE != kAny) {
+        if constexpr (!kDense) {
+          lds<E / 4>(from + i * Stage::kOne + GS::kBytes + E * lane, x.w);
+          x.sc = sc[i];
+        } else {
+          x.u = XS::finish(from + i * Stage::kOne + GS::kBytes, lane);
+          if (MODE == kPhase && !kEdges && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
+        }
       }
       return x;
     };
-    // aligned units are read from the ring again for dx; those of rows that start
-    // anywhere are kept, since putting them together costs shuffles
-    constexpr bool kKeep = MODE == kAny;
-    XUnit<TX, E> xu[kKeep ? NV : 1];
-    Unit<TG, E> gu[kKeep ? NV : 1];
+    auto x_normed = [&](int i, float* xh) {
+      if constexpr (MODE == kAny)
+        *xh = centered(i) * rstd;
+      else
+        x_unit(i).normed(p.saved.fmt, mean, rstd, xh);
+    };
+    auto x_affine = [&](int i, float a, float b, float* y) {
+      if constexpr (MODE == kAny)
+        *y = fmaf(centered(i), a, b);
+      else
+        x_unit(i).affine(p.saved.fmt, mean, a, b, y);
+    };
     float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
     float xe = 0.f, ge = 0.f;               // this lane's element of the row's ends: x - mean, and dy
     if constexpr (kEdges) {
@@ -274,14 +356,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
     for (int i = 0; i < NV; ++i) {
       float xh[E], dy[E], wu[E];
       w_unit(i, wu);
-      const XUnit<TX, E> xv = x_unit(i);
-      const Unit<TG, E> gv = g_unit(i);
-      if constexpr (kKeep) {
-        xu[i] = xv;
-        gu[i] = gv;
-      }
-      xv.normed(p.saved.fmt, mean, rstd, xh);
-      gv.get(dy);
+      x_normed(i, xh);
+      g_unit(i, dy);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int k = E * i + j;
@@ -323,13 +399,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
       for (int i = 0; i < NV; ++i) {
         float x[E], dy[E], wu[E];
         w_unit(i, wu);
-        if constexpr (kKeep) {
-          xu[i].affine(p.saved.fmt, mean, kd, k0, x);
-          gu[i].get(dy);
-        } else {
-          x_unit(i).affine(p.saved.fmt, mean, kd, k0, x);
-          g_unit(i).get(dy);
-        }
+        x_affine(i, kd, k0, x);
+        g_unit(i, dy);
 #pragma unroll
         for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * wu[j], rstd, x[j]);
         store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
@@ -367,7 +438,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         part[c] = s;
       }
     } else {
-      const bool wide = MODE != kPhase && (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
+      const bool wide = MODE == kAligned && (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (wide && cs.left(i) >= E) {
@@ -395,7 +466,9 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
   // two stages and the CTAs that then fit an SM: three stages take 84.2 us against
   // 82.8 on 16384 x 4096 bf16, and 150.8 against 129.6 in float32
   constexpr int S = 2;
-  constexpr int kStaged = SHAPE == kTall ? 4 * kWarpCols : 0, kMostWarps = SHAPE == kTall ? kTallWarps : kBwdWarps;
+  // the weights, or the elements of an 8-bit row that lies anywhere
+  constexpr int kStaged = SHAPE == kTall ? 4 * kWarpCols : (MODE == kAny && std::is_same_v<TX, Act8Tag> ? 128 * NV : 0);
+  constexpr int kMostWarps = SHAPE == kTall ? kTallWarps : kBwdWarps;
   constexpr int kWarp = (S * kStage > kGather ? S * kStage : kGather) + kStaged;
   auto* kernel = norm_bwd_kernel<TX, TG, SPAN, NV, E, S, MODE, SHAPE>;
   static NormHeld held;
@@ -426,7 +499,7 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
   if (cols <= 256) return norm_bwd_go<TX, TG, 8, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
   if (cols <= 512) return norm_bwd_go<TX, TG, 16, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
   if (cols <= 1024) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kLanes>(p, parts, occ, num_sms, s);
-  if constexpr (E == 8 && MODE != kAny) {
+  if constexpr (E == 8) {
     if (cols <= 1280) return norm_bwd_go<TX, TG, 32, 40 / E, E, MODE, kLanes>(p, parts, occ, num_sms, s);
   }
   if (cols <= kBwdWarps * kWarpCols) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCta>(p, parts, occ, num_sms, s);
@@ -434,7 +507,7 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
   // threads idle: from there one CTA of 16 warps has the row.  4000 rows of bf16:
   // 12288 columns 80.5 us against 86.2 in a cluster, 14336 from 8 bits 98.4 against
   // 123.8, 14335 118 against 157; 10240 columns 73.7 against 67.2.
-  if constexpr (E == 8 && MODE != kAny) {
+  if constexpr (E == 8) {
     if (cols > 10 * kWarpCols && cols <= kTallWarps * kWarpCols)
       return norm_bwd_go<TX, TG, 32, NV, E, MODE, kTall>(p, parts, occ, num_sms, s);
   }
@@ -447,8 +520,8 @@ int norm_bwd_kind(const NormBwdParams& p, int mode, bool narrow, int parts, bool
   constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kF32 = std::is_same_v<TX, float>;
   const bool g16 = p.g_dtype == METIS_BF16;
   if (mode == kAny)
-    return g16 ? norm_bwd_cols<TX, H, 8, kAny>(p, parts, occ, num_sms, s)
-               : norm_bwd_cols<TX, float, 8, kAny>(p, parts, occ, num_sms, s);
+    return g16 ? norm_bwd_cols<TX, H, 1, kAny>(p, parts, occ, num_sms, s)
+               : norm_bwd_cols<TX, float, 1, kAny>(p, parts, occ, num_sms, s);
   if constexpr (kDense) {
     if (mode == kPhase) {
       if constexpr (!kF32)

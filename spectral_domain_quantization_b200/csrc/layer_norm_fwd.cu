@@ -49,10 +49,9 @@ void launch_norm_fwd(const NormFwdParams& params, int dtype, int num_sms, cudaSt
   }
   const RowsOf m[2] = {{p.X, p.ldx, dtype}, {p.Y, p.ldy, p.y_dtype}};
   const int mode = norm_mode(m, 2, p.cols, true, 8, &p.period, &p.offset);
-  if (mode == kPhase && save) {
-    // the 8-bit blocks are columns of the matrix and the threads' columns are
-    // shifted: the copy is a kernel of its own (first, since Y may be X).  8192 x
-    // 4095 bf16: two kernels take less than one that puts each unit together.
+  if (mode != kAligned && save) {
+    // the 8-bit blocks are columns of the matrix and no lane has a whole word of
+    // one: the copy is a kernel of its own (first, since Y may be X)
     launch_act8_save(p.X, dtype, p.rows, p.cols, p.ldx, p.save, num_sms, s);
     save = false;
   }

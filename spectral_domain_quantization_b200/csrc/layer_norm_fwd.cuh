@@ -38,13 +38,32 @@ struct RowStats {
   }
 };
 
+// Warps of a CTA at most.  One element at a time takes more registers than 16 warps
+// have, so with kAny those are left to the rows that 12 do not hold (kTall): 8192 x
+// 4096 bf16 takes 51.3 us with 12 at most against 61.7 with 16, 4000 x 14336 takes 105
+// with 16 against 193 in a cluster.
+template <int MODE, int SHAPE>
+constexpr int fwd_warps = MODE == kAny && SHAPE != kTall ? 12 : 16;
+
+// Bytes of a warp's part of a row in the ring.
+template <typename T, int SPAN, int NV, int E, int MODE>
+struct FwdStage {
+  static constexpr int kBytes = NV * UnitSlot<T, E, MODE, 32>::kBytes;
+};
+template <typename T, int SPAN, int NV>
+struct FwdStage<T, SPAN, NV, 1, kAny> {
+  static constexpr int kBytes = RowImage<T, SPAN, NV>::kBytes;
+};
+
 template <typename T, int SPAN, int NV, int E, int S, int MODE, bool SAVE, int SHAPE>
-__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd_kernel(NormFwdParams p, int ctas) {
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warps<MODE, SHAPE>) norm_fwd_kernel(NormFwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
-  using Slot = UnitSlot<T, E, MODE, 32, SPAN>;
+  using Slot = UnitSlot<T, E, MODE, 32>;
+  using Image = RowImage<T, SPAN, NV>;            // kAny
   constexpr bool kRest = sizeof(T) == 4, CL = Cols::kClustered, kMulti = Cols::kMulti;
   constexpr bool kEdges = norm_edges<SPAN, MODE>;
-  constexpr int kSpan = SPAN, kStage = NV * Slot::kBytes;
+  constexpr int kSpan = SPAN, kStage = FwdStage<T, SPAN, NV, E, MODE>::kBytes;
+  static_assert(!SAVE || MODE == kAligned);
   using Ex = Exchange<kRest ? 3 : 2, SHAPE>;
   constexpr int kMost = Ex::kMost;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -64,13 +83,12 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
     if (SPAN < 32 || on) {
       const T* x = X + fetch_row * p.ldx;
       const bool inside = MODE == kPhase && on && row_inside(x, p.cols, span);
+      if constexpr (MODE == kAny) {
+        Image::start(into, lane, x + cs.col(0) - cs.t, on ? cs.left(0) + cs.t : 0, span);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t at = into + i * Slot::kBytes;
-        if constexpr (MODE == kAny)
-          Slot::start(at, lane, x + cs.col(i), on ? cs.left(i) : -16, cs.last, span);
-        else
-          Slot::start(at, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, span);
+        for (int i = 0; i < NV; ++i)
+          Slot::start(into + i * Slot::kBytes, lane, x + cs.col(i), on && cs.whole(i), on && cs.some(i), inside, span);
       }
     }
     cp_async_commit();
@@ -105,11 +123,11 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
   // all threads of a row leave the loop together; with several rows in a warp,
   // all of the warp
   for (int64_t row = cs.row; SPAN == 32 ? row < p.rows : row - (lane / SPAN) < p.rows; row += cs.step) {
+    if constexpr (MODE == kAny) __syncwarp();      // every lane has read the stage that is copied to
     fetch();
     const bool active = SPAN == 32 || row < p.rows;
     cp_async_wait<S - 1>();
     float v[NV * E], part[NV];
-    Unit<T, E> kept[MODE == kAny && SAVE ? NV : 1];
     float xe = 0.f;                         // this lane's element of the row's ends
     if constexpr (kEdges) {
       __syncwarp();                         // other lanes copied it
@@ -118,18 +136,23 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
       if (edge.first && lane == edge.first_owner) Slot::clear(from, lane);
       if (edge.last && lane == edge.last_owner) Slot::clear(from + edge.last_unit * Slot::kBytes, lane);
     }
+    uint32_t at = 0u;
+    if constexpr (MODE == kAny) {
+      const T* x = X + row * p.ldx + cs.col(0) - cs.t;
+      __syncwarp();                         // other lanes copied it
+      Image::end(from, lane, x, cs.left(0) + cs.t);
+      __syncwarp();
+      at = Image::place(from, lane, x);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const uint32_t at = from + i * Slot::kBytes;
-      Unit<T, E> u;
       if constexpr (MODE == kAny) {
-        u = Slot::finish(at, lane, X + row * p.ldx + cs.col(i), active ? cs.left(i) : 0, cs.last);
-        if constexpr (SAVE) kept[i] = u;
+        v[i] = Image::elem(at, i);
       } else {
-        u = Slot::finish(at, lane);
+        Unit<T, E> u = Slot::finish(from + i * Slot::kBytes, lane);
         if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
+        u.get(v + E * i);
       }
-      u.get(v + E * i);
       part[i] = tree_sum<E>(v + E * i);
     }
     if constexpr (kEdges) part[0] += xe;
@@ -141,7 +164,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
       float e[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
-      if (MODE != kAligned && !kEdges && !cs.whole(i)) {
+      if (MODE == kPhase && !kEdges && !cs.whole(i)) {
 #pragma unroll
         for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
       }
@@ -149,7 +172,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
 #pragma unroll
       for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
       if constexpr (kRest) p1[i] = tree_sum<E>(e);
-      if ((MODE == kAligned || kEdges) && !cs.whole(i)) {
+      if ((MODE != kPhase || kEdges) && !cs.whole(i)) {
         p2[i] = 0.f;
         if constexpr (kRest) p1[i] = 0.f;
       }
@@ -241,12 +264,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
       float x[NV][E];
       uint32_t codes[NV][E / 4];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if constexpr (MODE == kAny)
-          kept[i].get(x[i]);
-        else
-          Slot::finish(from + i * Slot::kBytes, lane).get(x[i]);
-      }
+      for (int i = 0; i < NV; ++i) Slot::finish(from + i * Slot::kBytes, lane).get(x[i]);
       const int pad = CL ? min(static_cast<int>(p.save.ldc), cs.lo + p.slice) : static_cast<int>(p.save.ldc);
       uint8_t* scales = p.save.scales + row * p.save.blocks;
       if constexpr (act8_dealt<E, NV>) {
@@ -289,19 +307,17 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 512) norm_fwd
   }
 }
 
-constexpr int kFwdWarps = 16;       // of a CTA
-
 template <typename T, int SPAN, int NV, int E, int MODE, bool SAVE, int SHAPE>
 void norm_fwd_go(const NormFwdParams& params, int num_sms, cudaStream_t s) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
-  constexpr int S = SHAPE == kLanes ? 3 : 2, kWarp = S * NV * UnitSlot<T, E, MODE, 32, SPAN>::kBytes;
+  constexpr int S = SHAPE == kLanes ? 3 : 2, kWarp = S * FwdStage<T, SPAN, NV, E, MODE>::kBytes;
   auto* kernel = norm_fwd_kernel<T, SPAN, NV, E, S, MODE, SAVE, SHAPE>;
   static NormHeld held;
   NormFwdParams p = params;
-  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), kFwdWarps);
+  const NormPlan plan(SHAPE, p.cols + (MODE == kPhase ? 7 : 0), fwd_warps<MODE, SHAPE>);
   p.slice = plan.slice;
   const int smem = plan.warps * kWarp;
-  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : kFwdWarps) * kWarp);
+  const int per_sm = held.get(kernel, plan.warps, smem, (SHAPE == kLanes ? 4 : fwd_warps<MODE, SHAPE>) * kWarp);
   const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX) / plan.ctas;
   const int64_t blocks = imin64((p.rows + Cols::kRows - 1) / Cols::kRows, imax64(1, most));
   launch_dependent(kernel, dim3(static_cast<unsigned>(norm_blocks(blocks, Cols::kRows, p.period) * plan.ctas)),
@@ -328,8 +344,10 @@ void norm_fwd_cols(const NormFwdParams& p, int num_sms, cudaStream_t s) {
     norm_fwd_go<T, 32, 40 / E, E, MODE, SAVE, kLanes>(p, num_sms, s);
   else if (cols <= 1536)
     norm_fwd_go<T, 32, 48 / E, E, MODE, SAVE, kLanes>(p, num_sms, s);
-  else if (cols <= kFwdWarps * kWarpCols)
+  else if (cols <= fwd_warps<MODE, kCta> * kWarpCols)
     norm_fwd_go<T, 32, NV, E, MODE, SAVE, kCta>(p, num_sms, s);
+  else if (MODE == kAny && cols <= fwd_warps<MODE, kTall> * kWarpCols)
+    norm_fwd_go<T, 32, NV, E, MODE, SAVE, MODE == kAny ? kTall : kCta>(p, num_sms, s);
   else
     norm_fwd_go<T, 32, NV, E, MODE, SAVE, kCluster>(p, num_sms, s);
 }

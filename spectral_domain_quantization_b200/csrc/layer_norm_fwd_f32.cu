@@ -6,7 +6,7 @@ namespace metis {
 void norm_fwd_f32(const NormFwdParams& p, int mode, bool save, int num_sms, cudaStream_t s) {
   using T = float;
   if (mode == kAny)
-    save ? norm_fwd_cols<T, 8, kAny, true>(p, num_sms, s) : norm_fwd_cols<T, 8, kAny, false>(p, num_sms, s);
+    norm_fwd_cols<T, 1, kAny, false>(p, num_sms, s);
   else if (mode == kPhase)
     norm_fwd_cols<T, 4, kPhase, false>(p, num_sms, s);
   else

@@ -317,20 +317,33 @@ MDEV void lds(uint32_t a, uint32_t* w) {
   }
 }
 
+template <typename T>
+MDEV float lds_elem(uint32_t a) {
+  if constexpr (sizeof(T) == 2) {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    return __bfloat162float(__ushort_as_bfloat16(h));
+  } else {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+    return f;
+  }
+}
+
 // How the rows of a matrix lie.
 enum RowMode {
   kAligned = 0,  // every unit of a row is one aligned word, and there is no part of a unit
   kPhase = 1,    // rows start anywhere, but all matrices of the call at the same element of a 16-byte (bf16: 8
                  // elements) period: a thread's columns are shifted so that its units are aligned words, a group
                  // of threads takes rows of one shift only, and only a row's first and last unit are in part outside
-  kAny = 2       // rows start anywhere: units are cut out of chunks (UnitLoad's way)
+  kAny = 2       // rows start anywhere: a warp's lanes take neighbouring elements, one at a time (RowImage)
 };
 
 // A unit's place in a stage of a ring: a thread copies what it will read itself
 // (cp.async), so the ring needs no barrier, and as many rows are on their way as
 // it has stages, whatever the registers hold.  One word of a thread, kThreads of
 // them in a row.
-template <typename T, int E, int MODE, int kThreads, int kSpan>
+template <typename T, int E, int MODE, int kThreads>
 struct UnitSlot {
   static constexpr int kWord = E * static_cast<int>(sizeof(T));
   static constexpr int kBytes = kWord * kThreads;
@@ -365,16 +378,7 @@ struct UnitSlot {
   }
   // element j of thread tid's unit, and zeros in the place of the unit
   static MDEV float elem(uint32_t base, int tid, int j) {
-    const uint32_t a = base + kWord * tid + static_cast<uint32_t>(sizeof(T)) * j;
-    if constexpr (sizeof(T) == 2) {
-      uint16_t h;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
-      return __bfloat162float(__ushort_as_bfloat16(h));
-    } else {
-      float f;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
-      return f;
-    }
+    return lds_elem<T>(base + kWord * tid + static_cast<uint32_t>(sizeof(T)) * j);
   }
   static MDEV void clear(uint32_t base, int tid) {
 #pragma unroll
@@ -383,51 +387,64 @@ struct UnitSlot {
   }
 };
 
-// kAny: the aligned chunks that the unit lies in, and one more for the last of
-// the row's lanes in a warp.
-template <typename T, int kThreads, int kSpan>
-struct UnitSlot<T, 8, kAny, kThreads, kSpan> {
-  static constexpr int kChunks = Unit<T>::kWords / 4;
+// kAny: the SPAN * NV elements of a row that SPAN lanes share, as they lie in memory
+// from the 16-byte chunk with the first of them on.  Lane t reads the elements
+// t, t + SPAN, ...: neighbouring lanes neighbouring elements, whatever the row's
+// alignment.  By whole warps; what one lane copied another reads, so a __syncwarp
+// goes before end(), between end() and elem(), and before the stage is copied to again.
+template <typename T, int SPAN, int NV>
+struct RowImage {
   static constexpr int kE = 16 / static_cast<int>(sizeof(T));
-  static constexpr int kExtra = 16 * (kThreads / kSpan);
-  static constexpr int kBytes = 16 * kThreads * kChunks + kExtra;
-  // `n`: elements left in the row from the unit's first
-  static MDEV void start(uint32_t base, int tid, const T* p, int n, bool last, const Span& s) {
-    const uintptr_t addr = reinterpret_cast<uintptr_t>(p);
-    const int sh = static_cast<int>(addr & 15u), se = sh / static_cast<int>(sizeof(T));
+  static constexpr int kChunks = NV / kE;                          // of a lane; one more for the last element
+  static constexpr int kOne = 16 * (SPAN * kChunks + 1);
+  static constexpr int kBytes = kOne * (32 / SPAN);                // of a warp
+  static_assert(NV % kE == 0 && SPAN >= kE - 1);
+  // `p`: the first element; `n` of them (0 or less: none) are the row's
+  static MDEV void start(uint32_t base, int lane, const T* p, int n, const Span& s) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15};
+    const uintptr_t end = n > 0 ? reinterpret_cast<uintptr_t>(p + n) : 0;
+    const int t = lane % SPAN;
+    base += kOne * (lane / SPAN);
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) chunk(base + 16 * (kThreads * k + tid), addr - sh + 16 * k, n + se > k * kE, s);
-    if (last)
-      chunk(base + 16 * (kThreads * kChunks + tid / kSpan), addr - sh + 16 * kChunks, sh != 0 && n + se > 8, s);
+    for (int k = 0; k < kChunks; ++k) chunk(base, a, t + SPAN * k, end, s);
+    if (t == 0) chunk(base, a, SPAN * kChunks, end, s);
   }
-  // the aligned chunk at `a`, zeros where it is not wanted or lies outside
-  static MDEV void chunk(uint32_t dst, uintptr_t a, bool want, const Span& s) {
-    if (want && a < s.lo) {                 // the matrix's first chunk: by element
+  // zeros from element n on, as far as the chunk with it reaches
+  static MDEV void end(uint32_t base, int lane, const T* p, int n) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) + n * static_cast<int>(sizeof(T));
+    const int at = off + lane % SPAN * static_cast<int>(sizeof(T));
+    if (n > 0 && n < SPAN * NV && at < (off + 15) / 16 * 16) put(base + kOne * (lane / SPAN) + at);
+  }
+  // the address of lane t's first element; the next ones are SPAN elements apart
+  static MDEV uint32_t place(uint32_t base, int lane, const T* p) {
+    return base + kOne * (lane / SPAN) + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u) +
+           static_cast<uint32_t>(sizeof(T)) * (lane % SPAN);
+  }
+  static MDEV float elem(uint32_t place, int i) {
+    return lds_elem<T>(place + static_cast<uint32_t>(sizeof(T)) * SPAN * i);
+  }
+
+ private:
+  // the aligned chunk k from `a` on, zeros where it is not wanted or lies outside
+  static MDEV void chunk(uint32_t base, uintptr_t a, int k, uintptr_t end, const Span& s) {
+    a += 16 * k;
+    const uint32_t dst = base + 16 * k;
+    if (a < end && a < s.lo) {              // the matrix's first chunk: by element
       uint32_t w[4];
       load_chunk<T>(a, s, w);
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                    : "memory");
     } else {
+      const bool want = a < end;
       const int bytes = want ? (s.hi - a < 16 ? static_cast<int>(s.hi - a) : 16) : 0;
       cp_async16(dst, reinterpret_cast<const void*>(want ? a : s.lo & ~uintptr_t{15}), bytes);
     }
   }
-  // by whole warps
-  static MDEV Unit<T> finish(uint32_t base, int tid, const T* p, int n, bool last) {
-    constexpr int kN = Unit<T>::kWords;
-    uint32_t in[kN + 4], x[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) lds16(base + 16 * (kThreads * k + tid), in + 4 * k);
-    if (last) lds16(base + 16 * (kThreads * kChunks + tid / kSpan), x);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, in[i], 1);
-      in[kN + i] = last ? x[i] : next;
-    }
-    Unit<T> u;
-    cut<T, kN>(in, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u), u.w);
-    if (n < 8) u.keep(0, n);
-    return u;
+  static MDEV void put(uint32_t a) {
+    if constexpr (sizeof(T) == 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
+    else
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(0u) : "memory");
   }
 };
 
