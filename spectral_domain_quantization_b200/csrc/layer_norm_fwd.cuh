@@ -9,6 +9,13 @@
 // a difference of large sums.  The row's mean stays a pair m0 + m1.  The grid is
 // no larger than what is resident at once, so a thread loads its columns' weight
 // and bias once for all its rows.
+//
+// Measured, bf16 unless said: 16384 x 4096 45.8 us, 5.9 TB/s (a copy does 6.55); 8192 x
+// 4096 24.9 us, float32 48.0 us, with the 8-bit copy 35.3 us (its arithmetic: 49 % more
+// instructions, two of three issue slots taken); 65536 x 1024 47.3 us; 4000 x 14336
+// 45.3 us; rows that start anywhere 65536 x 1001 46.9 us, 8192 x 4001 37.5 us (a third
+// more instructions than 4096 columns, and spilled registers); 8192 x 20000 285 us (a
+// barrier of two CTAs a row).
 #pragma once
 
 #include "layer_norm.cuh"

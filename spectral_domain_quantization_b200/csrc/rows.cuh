@@ -1,17 +1,19 @@
-// Units of 8 consecutive elements of a matrix row in registers, for rows that
-// start anywhere.
+// Consecutive elements of a matrix row ("units") in registers, for rows that start
+// anywhere.  Nothing outside the matrix is touched: what reaches over its first or
+// last byte is read by element.
 //
-// A warp's lanes hold consecutive units.  Where every row starts on a 16-byte
-// boundary a unit is one (bf16) or two (f32) 16-byte words.  Where it does not,
-// the lane still loads the aligned 16-byte chunks from the one its first element
-// lies in: the bytes behind its own chunks are the next lane's first chunk (a
-// shuffle; the last lane of a row's lanes loads that chunk itself), and the unit
-// is cut out of the two by a byte shift.  A store goes the other way round: a
-// lane writes the aligned chunk made of its predecessor's last bytes and its own
-// first; only the two ends of the lanes' run are written by element.  So a row of
-// any alignment moves as 16-byte words (3 to 4 times the rate of one element a
-// lane, measured on 4096 bf16 columns).  A chunk that reaches over the matrix's
-// first or last byte is read by element: nothing outside the matrix is touched.
+// In registers (UnitLoad, store_unit): a warp's lanes hold consecutive units of 8.
+// Where every row starts on a 16-byte boundary a unit is one (bf16) or two (f32)
+// 16-byte words.  Where it does not, the lane still loads the aligned 16-byte chunks
+// from the one its first element lies in: the bytes behind its own chunks are the next
+// lane's first chunk (a shuffle; the last lane of a row's lanes loads that chunk
+// itself), and the unit is cut out of the two by a byte shift.  A store goes the other
+// way round: a lane writes the aligned chunk made of its predecessor's last bytes and
+// its own first; only the two ends of the lanes' run are written by element.  8192 x
+// 4096 bf16 with rows 4097 apart go into 8 bits in 35 us so and come back in 39 (18.3
+// and 17.9 with rows 4096 apart): the shuffles and shifts are what is left.
+//
+// In shared memory (UnitSlot, RowImage): rows on their way in, copied asynchronously.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -211,54 +213,42 @@ struct UnitLoad<T, false> {
 
 // A unit on its way out, by whole warps.  `first`: no lane before this one holds
 // the row's previous unit.
-template <typename T, bool AL>
+template <typename T>
 MDEV void store_unit(T* p, const Unit<T>& u, int n, bool first, bool last) {
   constexpr int kN = Unit<T>::kWords;
   constexpr int kE = 16 / static_cast<int>(sizeof(T));
-  if constexpr (AL) {
-    if (n >= 8) {
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(p);
+  const int sh = static_cast<int>(addr & 15u), se = sh / static_cast<int>(sizeof(T));
+  uint32_t in[kN + 4], out[kN];
 #pragma unroll
-      for (int i = 0; i < kN / 4; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(u.w[4 * i], u.w[4 * i + 1], u.w[4 * i + 2], u.w[4 * i + 3]);
-    } else {
+  for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xFFFFFFFFu, u.w[kN - 4 + i], 1);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) p[j] = u.elem(j);
-    }
+  for (int i = 0; i < kN; ++i) in[4 + i] = u.w[i];
+  // byte 0 of the chunks is byte 16 - sh of `in` (all 16 of the predecessor's
+  // bytes are behind it when sh == 0)
+  if (sh == 0) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = u.w[i];
   } else {
-    const uintptr_t addr = reinterpret_cast<uintptr_t>(p);
-    const int sh = static_cast<int>(addr & 15u), se = sh / static_cast<int>(sizeof(T));
-    uint32_t in[kN + 4], out[kN];
+    cut<T, kN>(in, 16 - sh, out);
+  }
+  bool whole[kN / 4];                     // chunk k is written as one word
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xFFFFFFFFu, u.w[kN - 4 + i], 1);
+  for (int k = 0; k < kN / 4; ++k) {
+    whole[k] = n >= (k + 1) * kE - se && (k > 0 || sh == 0 || !first);
+    if (whole[k])
+      *reinterpret_cast<uint4*>(addr - sh + 16 * k) =
+          make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+  }
+  const bool next_whole = !last && n - 8 >= kE - se;   // the next lane writes this one's last elements
 #pragma unroll
-    for (int i = 0; i < kN; ++i) in[4 + i] = u.w[i];
-    // byte 0 of the chunks is byte 16 - sh of `in` (all 16 of the predecessor's
-    // bytes are behind it when sh == 0)
-    if (sh == 0) {
+  for (int j = 0; j < 8; ++j) {
+    const int k = (j + se) / kE;          // the chunk of element j
+    bool done = next_whole;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) out[i] = u.w[i];
-    } else {
-      cut<T, kN>(in, 16 - sh, out);
-    }
-    bool whole[kN / 4];                     // chunk k is written as one word
-#pragma unroll
-    for (int k = 0; k < kN / 4; ++k) {
-      whole[k] = n >= (k + 1) * kE - se && (k > 0 || sh == 0 || !first);
-      if (whole[k])
-        *reinterpret_cast<uint4*>(addr - sh + 16 * k) =
-            make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-    }
-    const bool next_whole = !last && n - 8 >= kE - se;   // the next lane writes this one's last elements
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = (j + se) / kE;          // the chunk of element j
-      bool done = next_whole;
-#pragma unroll
-      for (int q = 0; q < kN / 4; ++q)
-        if (k == q) done = whole[q];
-      if (j < n && !done) p[j] = u.elem(j);
-    }
+    for (int q = 0; q < kN / 4; ++q)
+      if (k == q) done = whole[q];
+    if (j < n && !done) p[j] = u.elem(j);
   }
 }
 
