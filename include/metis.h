@@ -500,8 +500,9 @@ METIS_API metis_status metis_act8_quantize_fp4(const metis_act8_tensor* in, int3
  *   saved   optional (NULL: none): X in 8 bits (metis_act8_tensor, rows x cols),
  *           the bytes metis_act8_save writes, from the same pass over X.
  * X, Y and ld need no more alignment than their elements; rows may be 0.
- * Statistics are float32 sums in a fixed order; neither the variance nor the
- * mean of a row far from zero is a difference of large sums.
+ * Statistics are float32 sums, in a fixed order that depends on the sizes, types,
+ * alignments and the device alone; neither the variance nor the mean of a row far
+ * from zero is a difference of large sums.
  * A row with an infinity or a NaN gives NaN in that row alone.  No workspace.
  * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtypes, eps, fmt), METIS_ERR_SHAPE,
  * METIS_ERR_ALIGN, METIS_ERR_UNSUPPORTED, METIS_ERR_CUDA.

@@ -394,6 +394,48 @@ def test_between_other_work():
         assert all(torch.equal(p, q) for p, q in zip(want, got))
 
 
+@pytest.mark.parametrize("cols", [130, 1001, 4001, 11003, 17001])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mxint8"])
+def test_special_rows_stay_alone(cols, pad, kind):
+    # rows next to one another in words, and matrices that lie differently
+    x, dy, w, b = data(12, cols, seed=50)
+    dt = "f32" if kind == "f32" else "bf16"
+    w, b = w.cuda(), b.cuda()
+    plain, dY = mat(x, dt, pad), mat(dy, dt)
+    bad = x.clone()
+    bad[2, 0], bad[5, cols - 1], bad[9, cols // 2] = float("inf"), float("nan"), float("-inf")
+    special = mat(bad, dt, pad)
+    rows = torch.tensor([2, 5, 9], device="cuda")
+    rest = torch.tensor([r for r in range(12) if r not in (2, 5, 9)], device="cuda")
+    fmt = kind if kind in act8_ref.FORMATS else None
+    got, want = api.layer_norm_fwd(special, w, b, save=fmt), api.layer_norm_fwd(plain, w, b, save=fmt)
+    assert torch.isnan(got.Y[rows]).all() and torch.equal(got.Y[rest], want.Y[rest])
+    dgot = api.layer_norm_bwd(dY, got.saved or special, got.mean, got.rstd, w)
+    dwant = api.layer_norm_bwd(dY, want.saved or plain, want.mean, want.rstd, w)
+    assert torch.isnan(dgot[0][rows]).all() and torch.equal(dgot[0][rest], dwant[0][rest])
+    assert torch.isnan(dgot[1]).all() and torch.equal(dgot[2], dwant[2])
+
+
+@pytest.mark.parametrize("cols", [130, 1001, 4001, 4096, 11003, 17001])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_in_place_of_another_lie(cols, dtype):
+    # dX over dY, X elsewhere against the words; and Y over X at every begin
+    x, dy, w, b = data(60, cols, seed=51)
+    X, dY, w, b = mat(x, dtype, 3, 1), mat(dy, dtype), w.cuda(), b.cuda()
+    r = api.layer_norm_fwd(X, w, b)
+    want = api.layer_norm_bwd(dY, X, r.mean, r.rstd, w)
+    over = dY.clone()
+    got = api.layer_norm_bwd(over, X, r.mean, r.rstd, w, out=over)
+    assert got[0] is over and all(torch.equal(p, q) for p, q in zip(got, want))
+    # (sums run in an order that depends on how the matrices lie: the same here)
+    Y = mat(x, dtype, 0, 5)
+    ref = api.layer_norm_fwd(mat(x, dtype, 0, 5), w, b, save="mxfp8", out=mat(x, dtype, 0, 5))
+    res = api.layer_norm_fwd(Y, w, b, save="mxfp8", out=Y)
+    check_fwd(res, mat(x, dtype, 0, 5), w, b)
+    assert torch.equal(Y, ref.Y) and torch.equal(res.saved.codes, ref.saved.codes)
+
+
 def test_offsets_past_32_bits():
     # 2.3e9 elements: the rows at the end against the same rows alone
     rows, cols, tail = 70000, 32768, 40
