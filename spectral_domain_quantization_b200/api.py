@@ -232,25 +232,11 @@ def _call_with_workspace(fn, args_before_ws, args_after_ws, device, what, worksp
 # FP4 tensors
 # --------------------------------------------------------------------------
 
-_ones = {}
-
-
-def _one(device):
-    """A float32 1 on `device` that nothing writes (MXFP4 has no tensor scale)."""
-    t = _ones.get(device)
-    if t is None:
-        t = torch.ones(1, dtype=torch.float32, device=device)
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(device).synchronize()     # other streams may read it
-            _ones[device] = t
-    return t
-
-
 class QTensor:
     """An FP4 matrix (outer x inner, blocks along inner) held in torch buffers."""
 
     def __init__(self, fmt, outer, inner, device="cuda", linear=False, inner_sum=False, written=False):
-        # written: the call this is made for writes tensor_scale (NVFP4)
+        # written: the call this is made for writes tensor_scale
         L = lib()
         self.fmt = FMT[fmt]
         self.outer, self.inner = int(outer), int(inner)
@@ -261,12 +247,8 @@ class QTensor:
                                   dtype=torch.uint8, device=device)
         self.scales_linear = (torch.empty(self.outer * (self.inner // self.block), dtype=torch.uint8,
                                           device=device) if linear else None)
-        if not written:
-            self.tensor_scale = torch.ones(1, dtype=torch.float32, device=device)
-        elif self.fmt == NVFP4:
-            self.tensor_scale = torch.empty(1, dtype=torch.float32, device=device)
-        else:
-            self.tensor_scale = _one(self.codes.device)
+        make = torch.empty if written else torch.ones
+        self.tensor_scale = make(1, dtype=torch.float32, device=device)
         self.inner_sum = torch.empty(self.outer, dtype=torch.float32, device=device) if inner_sum else None
 
     def struct(self):
@@ -288,7 +270,8 @@ def quantize_fp4(X, fmt, axis=1, sub_col=None, linear=False, inner_sum=False, ou
     rows, cols = X.shape
     outer, inner = (rows, cols) if axis == 1 else (cols, rows)
     if out is None:
-        out = QTensor(fmt, outer, inner, X.device, linear=linear, inner_sum=inner_sum, written=True)
+        out = QTensor(fmt, outer, inner, X.device, linear=linear, inner_sum=inner_sum,
+                      written=FMT[fmt] == NVFP4)
     s = out.struct()
     L = lib()
     _call_with_workspace(

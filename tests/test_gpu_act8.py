@@ -178,3 +178,17 @@ def test_refusals():
             call()
     with pytest.raises(TypeError):
         api.restore_act8(a, torch.float16)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_tensor_scale_is_the_results_own(fmt):
+    # writing one result's scale reaches no other
+    X = torch.randn(64, 96, device="cuda")
+    a = api.save_act8(X)
+    first = [api.quantize_fp4_act8(a, fmt, 0), api.quantize_fp4(X, fmt, 0)]
+    want = [float(q.tensor_scale) for q in first]
+    assert fmt == "nv" or want == [1.0, 1.0]
+    for q in first:
+        q.tensor_scale.fill_(7)
+    second = [api.quantize_fp4_act8(a, fmt, 0), api.quantize_fp4(X, fmt, 0)]
+    assert [float(q.tensor_scale) for q in second] == want
