@@ -477,8 +477,7 @@ METIS_API metis_status metis_act8_restore(const metis_act8_tensor* in, void* Y, 
  *       of a forward product); 0: blocks along the rows (out: cols x rows; the
  *       left operand X^T of dW = X^T dY).  The blocked dimension must be a
  *       multiple of 32, and neither dimension more than 2^36.
- *   out  codes, scales, tensor_scale (METIS_MXFP4: 1, or NULL) and, optionally,
- *       scales_linear;
+ *   out  codes, scales, tensor_scale and, optionally, scales_linear;
  *       out->inner_sum must be NULL (METIS_ERR_UNSUPPORTED).
  * Errors otherwise as for metis_quantize_fp4.  No workspace.
  */

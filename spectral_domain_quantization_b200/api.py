@@ -6,6 +6,7 @@ CUDA stream; every arithmetic step runs in the CUDA kernels of
 device is not sm_100, calls raise.
 """
 import ctypes
+import functools
 import os
 import re
 
@@ -232,32 +233,70 @@ def _call_with_workspace(fn, args_before_ws, args_after_ws, device, what, worksp
 # FP4 tensors
 # --------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=4096)
+def _fp4_bytes(fmt, outer, inner):
+    """Bytes of an FP4 matrix's codes and scales."""
+    L = lib()
+    return L.metis_fp4_codes_bytes(outer, inner), L.metis_fp4_scales_bytes(fmt, outer, inner)
+
+
 class QTensor:
-    """An FP4 matrix (outer x inner, blocks along inner) held in torch buffers."""
+    """An FP4 matrix (outer x inner, blocks along inner) held in torch buffers:
+    codes, scales and tensor_scale (1 for MXFP4), and scales_linear and inner_sum
+    or None."""
 
     def __init__(self, fmt, outer, inner, device="cuda", linear=False, inner_sum=False, written=False):
-        # written: the call this is made for writes tensor_scale
-        L = lib()
+        # written: for a call that writes all of it now.  codes, scales and
+        # tensor_scale are then parts of one buffer, and tensors when asked for
         self.fmt = FMT[fmt]
         self.outer, self.inner = int(outer), int(inner)
         self.block = 32 if self.fmt == MXFP4 else 16
-        self.codes = torch.empty(L.metis_fp4_codes_bytes(self.outer, self.inner), dtype=torch.uint8,
-                                 device=device)
-        self.scales = torch.empty(L.metis_fp4_scales_bytes(self.fmt, self.outer, self.inner),
-                                  dtype=torch.uint8, device=device)
+        nc, ns = _fp4_bytes(self.fmt, self.outer, self.inner)
+        if written:
+            at = (nc + 255) // 256 * 256
+            end = (at + ns + 255) // 256 * 256
+            self._parts = (nc, at, ns, end)
+            self._buf = torch.empty(end + 4, dtype=torch.uint8, device=device)
+            self.device = self._buf.device
+        else:
+            self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
+            self.scales = torch.empty(ns, dtype=torch.uint8, device=device)
+            self.tensor_scale = torch.ones(1, dtype=torch.float32, device=device)
+            self.device = self.codes.device
         self.scales_linear = (torch.empty(self.outer * (self.inner // self.block), dtype=torch.uint8,
                                           device=device) if linear else None)
-        make = torch.empty if written else torch.ones
-        self.tensor_scale = make(1, dtype=torch.float32, device=device)
         self.inner_sum = torch.empty(self.outer, dtype=torch.float32, device=device) if inner_sum else None
+
+    def __getattr__(self, name):
+        # reached for what is not set yet
+        if name in ("codes", "scales", "tensor_scale") and "_buf" in self.__dict__:
+            nc, at, ns, end = self._parts
+            if name == "codes":
+                self.codes = self._buf[:nc]
+            elif name == "scales":
+                self.scales = self._buf[at:at + ns]
+            elif self.fmt == NVFP4:
+                self.tensor_scale = self._buf[end:].view(torch.float32)
+            else:
+                self.tensor_scale = torch.ones(1, dtype=torch.float32, device=self.device)
+            return self.__dict__[name]
+        raise AttributeError(name)
 
     def struct(self):
         s = FP4Struct()
         s.fmt, s.outer, s.inner = self.fmt, self.outer, self.inner
-        s.codes = self.codes.data_ptr()
-        s.scales = self.scales.data_ptr()
+        has = self.__dict__
+        if "_buf" in has:
+            base, (_, at, _, end) = self._buf.data_ptr(), self._parts
+            s.codes, s.scales = base, base + at
+            s.tensor_scale = base + end if self.fmt == NVFP4 else None
+        if "codes" in has:
+            s.codes = self.codes.data_ptr()
+        if "scales" in has:
+            s.scales = self.scales.data_ptr()
+        if "tensor_scale" in has:
+            s.tensor_scale = self.tensor_scale.data_ptr()
         s.scales_linear = self.scales_linear.data_ptr() if self.scales_linear is not None else None
-        s.tensor_scale = self.tensor_scale.data_ptr()
         s.inner_sum = self.inner_sum.data_ptr() if self.inner_sum is not None else None
         self._s = s          # keep alive while pointers are in use
         return s
@@ -271,7 +310,7 @@ def quantize_fp4(X, fmt, axis=1, sub_col=None, linear=False, inner_sum=False, ou
     outer, inner = (rows, cols) if axis == 1 else (cols, rows)
     if out is None:
         out = QTensor(fmt, outer, inner, X.device, linear=linear, inner_sum=inner_sum,
-                      written=FMT[fmt] == NVFP4)
+                      written=True)
     s = out.struct()
     L = lib()
     _call_with_workspace(
@@ -337,7 +376,7 @@ def _out_dtype(dt):
 
 def linear_fwd(X, W, M, N, K, out_dtype=torch.float32, Y=None, dev_status=None):
     """Y = X W on FP4 operands (metis_linear_fwd).  X, W: Operand."""
-    dev = X.R.codes.device
+    dev = X.R.device
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=dev)
     if dev_status is None:
@@ -353,7 +392,7 @@ def linear_fwd(X, W, M, N, K, out_dtype=torch.float32, Y=None, dev_status=None):
 def linear_bwd(dY_n, Wt, Xt, dY_m, M, N, K, out_dtype=torch.float32, dX=None, dW=None,
                want_dx=True, want_dw=True, dev_status=None):
     """dX = dY W^T and dW = X^T dY on FP4 operands (metis_linear_bwd)."""
-    dev = (dY_n or Xt).R.codes.device
+    dev = (dY_n or Xt).R.device
     if want_dx and dX is None:
         dX = torch.empty((M, K), dtype=out_dtype, device=dev)
     if want_dw and dW is None:
@@ -733,7 +772,7 @@ def quantize_fp4_act8(a, fmt, axis=1, linear=False, out=None):
         raise ValueError(f"the blocked dimension must be a multiple of 32 (it is {inner}) and no dimension 0")
     if out is None:
         out = QTensor(fmt, outer, inner, a.device, linear=linear, written=True)
-    elif (out.fmt, out.outer, out.inner) != (FMT[fmt], outer, inner) or out.codes.device != a.device:
+    elif (out.fmt, out.outer, out.inner) != (FMT[fmt], outer, inner) or out.device != a.device:
         raise ValueError(f"out must be a QTensor of {outer} x {inner} on {a.device}")
     _run_on(a.device, lib().metis_act8_quantize_fp4, "metis_act8_quantize_fp4",
             ctypes.byref(a._s), axis, ctypes.byref(out.struct()))

@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantPar
     for (int i = tid; i < METIS_ACT8_AMAX; i += kThreads) m = fmaxf(m, p.in.amax[i]);
     s_t = nv_tensor_scale(cta_max(m));
     nv_enc_table(s_t, enc_tab);
+    if (blockIdx.x == 0 && tid == 0) *p.tensor_scale = s_t;
     __syncthreads();
   }
-  if (blockIdx.x == 0 && tid == 0 && p.tensor_scale) *p.tensor_scale = s_t;    // 1 for MXFP4
   const NvScale nv(s_t);
   Tile tile(p);
   // axis 0: a warp's block of kBlk rows x 128 bytes of the next tile is on its way
