@@ -470,8 +470,8 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   constexpr int kStage = BwdStage<TX, TG, SPAN, NV, E, MODE>::kBytes;
   constexpr int kGather = SHAPE == kLanes && Cols::kRows > 1 ? 32 * NV * E * 4 : 0;   // of a warp, when the ring is done
-  // two stages and the CTAs that then fit an SM: three stages take 84.2 us against
-  // 82.8 on 16384 x 4096 bf16, and 150.8 against 129.6 in float32
+  // two stages and the CTAs that then fit an SM: three stages take 78.6 us against
+  // 77.1 on 16384 x 4096 bf16, and 144 against 126 in float32
   constexpr int S = 2;
   // the weights, or the elements of an 8-bit row that lies anywhere
   constexpr int kStaged = SHAPE == kTall ? 4 * kWarpCols : (MODE == kAny && std::is_same_v<TX, Act8Tag> ? 128 * NV : 0);
@@ -496,7 +496,7 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
 
 // E columns a unit, 32 a thread (16 where a row has 64 or fewer; 40 where that saves
 // the row's second warp and its sums still fit the registers: 16384 x 1280 bf16 takes
-// 34.0 us so against 44.6, 16384 x 1027 47 against 58).
+// 30.1 us so against 40.9, 16384 x 1027 41.7 against 54.0).
 template <typename TX, typename TG, int E, int MODE>
 int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cudaStream_t s) {
   constexpr int NV = 32 / E, L = E == 8 ? 4 : 8;
