@@ -17,6 +17,7 @@
 #include "act8.cuh"
 #include "dependent.cuh"
 #include "layer_norm.h"
+#include "pairs.cuh"
 #include "rows.cuh"
 
 namespace metis {

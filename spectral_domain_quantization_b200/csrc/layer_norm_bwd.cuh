@@ -8,12 +8,13 @@
 // sees, so dw and db are running sums in its registers; a CTA's rows end as one
 // row of partial sums, and a second kernel adds those in a fixed order.
 //
-// Measured, bf16 unless said: 16384 x 4096 77.0 us, 5.2 TB/s (a copy does 6.55), float32
-// 126 us (6.4 TB/s), from 8 bits with a float32 gradient 106 us (5.7 TB/s); 65536 x 1024
-// 72.5 us; 4000 x 14336 89 us; rows that start anywhere 65536 x 1001 92.8 us, 8192 x
-// 4001 62.8 us; matrices that lie differently 8192 x 4096 91 us.  Where it is short of
-// the copy's rate, 63 to 67 % of the issue slots are taken with 12 to 16 warps an SM:
-// the sums of 32 columns a thread take 64 registers, and the weights 32.
+// Measured, bf16 unless said: 16384 x 4096 77.3 us, 5.2 TB/s (a copy does 6.55), float32
+// 126 us (6.4 TB/s), from 8 bits with a float32 gradient 98.8 us (6.1 TB/s); 8192 x 4096
+// from 8 bits 42.8 us; 65536 x 1024 72.2 us; 4000 x 14336 89 us; rows that start anywhere
+// 65536 x 1001 86.9 us, 8192 x 4001 58.7 us; matrices that lie differently 8192 x 4096
+// 66.3 us.  The arithmetic goes two columns an instruction (pairs.cuh); what is left
+// short of the copy's rate waits for rows with 12 to 16 warps an SM, since the sums of
+// 32 columns a thread take 64 registers and the weights 32.
 #pragma once
 
 #include "layer_norm.cuh"
@@ -36,19 +37,12 @@ struct XBytes<Act8Tag, E, MODE> {
 template <typename TX, int E>
 struct XUnit {
   Unit<TX, E> u;
-  // (x - mean) rstd
-  MDEV void normed(int, float mean, float rstd, float* xh) const {
+  // x - mean, for the negative mean twice
+  MDEV void centered(int, f32x2 minus, f32x2* d) const {
     float x[E];
     u.get(x);
 #pragma unroll
-    for (int j = 0; j < E; ++j) xh[j] = (x[j] - mean) * rstd;
-  }
-  // (x - mean) a + b
-  MDEV void affine(int, float mean, float a, float b, float* y) const {
-    float x[E];
-    u.get(x);
-#pragma unroll
-    for (int j = 0; j < E; ++j) y[j] = fmaf(x[j] - mean, a, b);
+    for (int k = 0; k < E / 2; ++k) d[k] = add2(pair(x[2 * k], x[2 * k + 1]), minus);
   }
 };
 // 8 bits: an element is a small integer (or E4M3) times the block's power of two,
@@ -57,29 +51,19 @@ template <int E>
 struct XUnit<Act8Tag, E> {
   uint32_t w[E / 4];
   uint32_t sc;      // scale code
-  MDEV void centered(int fmt, float mean, float* d) const {
-    float f;
+  MDEV void centered(int fmt, f32x2 minus, f32x2* d) const {
+    float f, x[E];
     if (fmt == METIS_MXINT8) {
       f = act8_factor<METIS_MXINT8>(sc);
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXINT8>(w[k], d + 4 * k);
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXINT8>(w[k], x + 4 * k);
     } else {
       f = act8_factor<METIS_MXFP8>(sc);
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXFP8>(w[k], d + 4 * k);
+      for (int k = 0; k < E / 4; ++k) act8_elems4<METIS_MXFP8>(w[k], x + 4 * k);
     }
 #pragma unroll
-    for (int j = 0; j < E; ++j) d[j] = fmaf(d[j], f, -mean);
-  }
-  MDEV void normed(int fmt, float mean, float rstd, float* xh) const {
-    centered(fmt, mean, xh);
-#pragma unroll
-    for (int j = 0; j < E; ++j) xh[j] *= rstd;
-  }
-  MDEV void affine(int fmt, float mean, float a, float b, float* y) const {
-    centered(fmt, mean, y);
-#pragma unroll
-    for (int j = 0; j < E; ++j) y[j] = fmaf(y[j], a, b);
+    for (int k = 0; k < E / 2; ++k) d[k] = fma2(pair(x[2 * k], x[2 * k + 1]), pair(f), minus);
   }
 };
 
@@ -112,8 +96,12 @@ struct BwdStage<Act8Tag, TG, SPAN, NV, 1, kAny> {
 constexpr int kBwdWarps = 8;       // of a CTA
 constexpr int kTallWarps = 16;
 
+// (Aligned bf16 rows of a CTA are held to 128 registers, four CTAs of 4096 columns an
+// SM: 4096 x 8192 takes 47.4 us so against 62.5 with 148 registers.)
 template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, int SHAPE>
-__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256)) norm_bwd_kernel(NormBwdParams p, int ctas) {
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256),
+                                  SHAPE == kCta && MODE == kAligned && E == 8 && !std::is_same_v<TX, Act8Tag> ? 2 : 0)
+    norm_bwd_kernel(NormBwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
   using GS = UnitSlot<TG, E, MODE, 32>;
@@ -125,6 +113,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   constexpr bool kDense = !std::is_same_v<TX, Act8Tag>, kMulti = Cols::kMulti, CL = Cols::kClustered;
   constexpr bool kEdges = norm_edges<SPAN, MODE>;
   constexpr int kSpan = SPAN, kMost = Ex::kMost, kOwn = NV * E, kStage = Stage::kBytes;
+  constexpr int G = E == 1 ? 2 : E;              // columns that are worked on together: a unit, or two of one column
   static_assert(kDense || MODE != kPhase, "the 8-bit blocks are columns of the matrix: no shift");
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float parts[Ex::kFloats];
@@ -208,8 +197,13 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch();
   fetch_stats(cs.row);
-  float w[kOwn], aw[kOwn], ab[kOwn];
-  load_vector(cs, p.w, p.w_dtype, 1.f, w);
+  f32x2 w[kOwn / 2], aw[kOwn / 2], ab[kOwn / 2];
+  {
+    float v[kOwn];
+    load_vector(cs, p.w, p.w_dtype, 1.f, v);
+#pragma unroll
+    for (int k = 0; k < kOwn / 2; ++k) w[k] = pair(v[2 * k], v[2 * k + 1]);
+  }
   // kTall: 128 registers a thread have no room for the weights; each thread keeps
   // its own behind the ring
   constexpr bool kStaged = SHAPE == kTall;
@@ -217,24 +211,24 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   if constexpr (kStaged) {
 #pragma unroll
     for (int k = 0; k < kOwn / 4; ++k)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * k * blockDim.x), "f"(w[4 * k]),
-                   "f"(w[4 * k + 1]), "f"(w[4 * k + 2]), "f"(w[4 * k + 3])
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(w_at + 16 * k * blockDim.x), "l"(w[2 * k]), "l"(w[2 * k + 1])
                    : "memory");
   }
-  auto w_unit = [&](int i, float* o) {
+  auto w_group = [&](int i, f32x2* o) {
     if constexpr (kStaged) {
-      uint32_t u[E];
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k) lds16(w_at + 16 * (i * (E / 4) + k) * blockDim.x, u + 4 * k);
-#pragma unroll
-      for (int j = 0; j < E; ++j) o[j] = __uint_as_float(u[j]);
+      for (int k = 0; k < G / 4; ++k)
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                     : "=l"(o[2 * k]), "=l"(o[2 * k + 1])
+                     : "r"(w_at + 16 * (i * (G / 4) + k) * blockDim.x)
+                     : "memory");
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) o[j] = w[E * i + j];
+      for (int j = 0; j < G / 2; ++j) o[j] = w[G / 2 * i + j];
     }
   };
 #pragma unroll
-  for (int k = 0; k < kOwn; ++k) aw[k] = ab[k] = 0.f;
+  for (int k = 0; k < kOwn / 2; ++k) aw[k] = ab[k] = pair(0.f);
   const NormEdge edge(cs);
   const float we = kEdges && edge.on && p.w ? load_any(p.w, p.w_dtype, edge.col) : 1.f;
   float awe = 0.f, abe = 0.f;             // dw and db of that element's column
@@ -291,28 +285,29 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         x_at = wide + 4 * cs.t;
       }
     }
-    // dy of unit i, and (x - mean) a + b or (x - mean) rstd
-    auto g_unit = [&](int i, float* dy) {
+    // dy and x - mean of group i
+    const f32x2 minus = pair(-mean);
+    auto g_group = [&](int i, f32x2* dy) {
+      float v[G];
       if constexpr (MODE == kAny) {
-        *dy = GI::elem(g_at, i);
+        v[0] = GI::elem(g_at, 2 * i);
+        v[1] = GI::elem(g_at, 2 * i + 1);
       } else {
         Unit<TG, E> u = GS::finish(from + i * Stage::kOne, lane);
         if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
-        u.get(dy);
+        u.get(v);
       }
+#pragma unroll
+      for (int k = 0; k < G / 2; ++k) dy[k] = pair(v[2 * k], v[2 * k + 1]);
     };
-    auto centered = [&](int i) {
-      if constexpr (MODE != kAny) {
-        return 0.f;                         // (not called)
-      } else if constexpr (kDense) {
-        return XI::elem(x_at, i) - mean;
+    auto x_group = [&](int i, f32x2* d) {
+      if constexpr (MODE == kAny) {
+        if constexpr (kDense)
+          *d = add2(pair(XI::elem(x_at, 2 * i), XI::elem(x_at, 2 * i + 1)), minus);
+        else
+          *d = pair(lds_elem<float>(x_at + 8 * SPAN * i), lds_elem<float>(x_at + 8 * SPAN * i + 4 * SPAN));
       } else {
-        return lds_elem<float>(x_at + 4 * SPAN * i);
-      }
-    };
-    auto x_unit = [&](int i) {
-      XUnit<TX, MODE == kAny ? 4 : E> x;
-      if constexpr (MODE != kAny) {
+        XUnit<TX, E> x;
         if constexpr (!kDense) {
           lds<E / 4>(from + i * Stage::kOne + GS::kBytes + E * lane, x.w);
           x.sc = sc[i];
@@ -320,20 +315,8 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
           x.u = XS::finish(from + i * Stage::kOne + GS::kBytes, lane);
           if (MODE == kPhase && !kEdges && !cs.whole(i)) x.u.keep(cs.lo - cs.col(i), cs.left(i));
         }
+        x.centered(p.saved.fmt, minus, d);
       }
-      return x;
-    };
-    auto x_normed = [&](int i, float* xh) {
-      if constexpr (MODE == kAny)
-        *xh = centered(i) * rstd;
-      else
-        x_unit(i).normed(p.saved.fmt, mean, rstd, xh);
-    };
-    auto x_affine = [&](int i, float a, float b, float* y) {
-      if constexpr (MODE == kAny)
-        *y = fmaf(centered(i), a, b);
-      else
-        x_unit(i).affine(p.saved.fmt, mean, a, b, y);
     };
     float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
     float xe = 0.f, ge = 0.f;               // this lane's element of the row's ends: x - mean, and dy
@@ -359,22 +342,26 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
       awe = fmaf(ge, xh, awe);
       abe += ge;
     }
+    f32x2 t1 = pair(s1, 0.f), t2 = pair(s2, 0.f);
+    const f32x2 rr = pair(rstd);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float xh[E], dy[E], wu[E];
-      w_unit(i, wu);
-      x_normed(i, xh);
-      g_unit(i, dy);
+    for (int i = 0; i < kOwn / G; ++i) {
+      f32x2 d[G / 2], dy[G / 2], wu[G / 2];
+      w_group(i, wu);
+      x_group(i, d);
+      g_group(i, dy);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int k = E * i + j;
-        const float gk = dy[j] * wu[j];
-        s1 = fmaf(gk, xh[j], s1);
-        s2 += gk;
-        aw[k] = fmaf(dy[j], xh[j], aw[k]);
-        ab[k] += dy[j];
+      for (int j = 0; j < G / 2; ++j) {
+        const int k = G / 2 * i + j;
+        const f32x2 xh = mul2(d[j], rr), gk = mul2(dy[j], wu[j]);
+        t1 = fma2(gk, xh, t1);
+        t2 = add2(t2, gk);
+        aw[k] = fma2(dy[j], xh, aw[k]);
+        ab[k] = add2(ab[k], dy[j]);
       }
     }
+    s1 = pair_sum(t1);
+    s2 = pair_sum(t2);
     if (p.dX) {
       float c1, c2;
       if constexpr (!kMulti) {
@@ -402,15 +389,19 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
       // dx = rstd g + (x - mean) kd + k0
       const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -rstd * (c2 * p.inv_n);
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
+      const f32x2 kd2 = pair(kd), k02 = pair(k0);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float x[E], dy[E], wu[E];
-        w_unit(i, wu);
-        x_affine(i, kd, k0, x);
-        g_unit(i, dy);
+      for (int i = 0; i < kOwn / G; ++i) {
+        f32x2 d[G / 2], dy[G / 2], wu[G / 2];
+        float o[G];
+        w_group(i, wu);
+        x_group(i, d);
+        g_group(i, dy);
 #pragma unroll
-        for (int j = 0; j < E; ++j) dy[j] = fmaf(dy[j] * wu[j], rstd, x[j]);
-        store_row_unit_any(cs, out, p.dx_dtype, dy, i, active);
+        for (int j = 0; j < G / 2; ++j)
+          unpair(fma2(mul2(dy[j], wu[j]), rr, fma2(d[j], kd2, k02)), o[2 * j], o[2 * j + 1]);
+        store_row_unit_any(cs, out, p.dx_dtype, o, G / E * i, active);
+        if constexpr (E == 1) store_row_unit_any(cs, out, p.dx_dtype, o + 1, 2 * i + 1, active);
       }
       if constexpr (kEdges) {
         if (edge.on) store_any(out, p.dx_dtype, edge.col, fmaf(ge * we, rstd, fmaf(xe, kd, k0)));
@@ -428,7 +419,9 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
     float* part = which == 0 ? p.part_w : p.part_b;
     if (!part) continue;
     part += blk * p.part_ld;
-    const float* a = which == 0 ? aw : ab;
+    float a[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn / 2; ++k) unpair(which == 0 ? aw[k] : ab[k], a[2 * k], a[2 * k + 1]);
     if constexpr (Cols::kRows > 1) {
       __syncthreads();
 #pragma unroll
@@ -512,7 +505,7 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
   if (cols <= kBwdWarps * kWarpCols) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCta>(p, parts, occ, num_sms, s);
   // A cluster's CTAs of more than 5 warps leave an SM room for one, and half its
   // threads idle: from there one CTA of 16 warps has the row, where the arithmetic is
-  // what bounds it.  4000 rows from 8 bits: 14336 columns 98.7 us against 123.7 in a
+  // what bounds it.  4000 rows from 8 bits: 14336 columns 94.5 us against 123.7 in a
   // cluster, 10240 columns 82.6 against 77.1; bf16 14335 columns 113 against 157, 8449
   // columns 92.3 against 90.2.  (bf16 that lies aligned: 94.6 against 89.1 with 14336.)
   if constexpr (E == 8 && (MODE == kPhase || std::is_same_v<TX, Act8Tag>)) {

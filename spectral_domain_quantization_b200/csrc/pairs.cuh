@@ -1,0 +1,43 @@
+// Two float32 values in a 64-bit register pair, and the arithmetic that takes both
+// in one instruction (each rounded as by itself): where the issue slots bind, half
+// the instructions.  Layer norm backward, 8192 x 4096: from 8 bits 47.0 -> 42.8 us,
+// bf16 matrices that lie differently 91.2 -> 66.3 us, 8192 x 4001 62.9 -> 58.7 us.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace metis {
+
+using f32x2 = uint64_t;
+
+MDEV f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MDEV f32x2 pair(float both) { return pair(both, both); }
+MDEV void unpair(f32x2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+MDEV float pair_sum(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
+}
+MDEV f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MDEV f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MDEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+}  // namespace metis
