@@ -208,27 +208,6 @@ MDEV float inv_sqrt(float a) {
   return fabsf(e) < 0.5f ? fmaf(0.5f * y, e, y) : y;   // a of 0, infinity or NaN: as it is
 }
 
-// Sum of N values (a power of two) in a balanced tree: a value passes through
-// log2 N additions, so an outlier does not cost the values after it their bits.
-template <int N>
-MDEV float tree_sum(const float* v) {
-  if constexpr (N == 1) {
-    return v[0];
-  } else {
-    return tree_sum<N / 2>(v) + tree_sum<N / 2>(v + N / 2);
-  }
-}
-
-// The same of any number of values.
-template <int N>
-MDEV float tree_sum_any(const float* v) {
-  constexpr int kHead = N >= 8 ? 8 : (N >= 4 ? 4 : (N >= 2 ? 2 : 1));
-  if constexpr (N == kHead)
-    return tree_sum<N>(v);
-  else
-    return tree_sum<kHead>(v) + tree_sum_any<N - kHead>(v + kHead);
-}
-
 // Sums over a warp of two values at once: in the first step a lane passes on the
 // one it does not keep.  Lanes 0 to 15 end with the sum of a, the others with b's.
 MDEV float warp_sums2(float a, float b) {

@@ -10,12 +10,12 @@
 // no larger than what is resident at once, so a thread loads its columns' weight
 // and bias once for all its rows.
 //
-// Measured, bf16 unless said: 16384 x 4096 45.8 us, 5.9 TB/s (a copy does 6.55); 8192 x
-// 4096 24.9 us, float32 48.0 us, with the 8-bit copy 35.3 us (its arithmetic: 49 % more
-// instructions, two of three issue slots taken); 65536 x 1024 47.3 us; 4000 x 14336
-// 45.3 us; rows that start anywhere 65536 x 1001 46.9 us, 8192 x 4001 37.5 us (a third
-// more instructions than 4096 columns, and spilled registers); 8192 x 20000 285 us (a
-// barrier of two CTAs a row).
+// Measured, bf16 unless said: 16384 x 4096 44.9 us, 6.0 TB/s (a copy does 6.55); 8192 x
+// 4096 24.5 us, float32 49.0 us, with the 8-bit copy 34.7 us (its arithmetic takes the
+// issue slots); 65536 x 1024 48.6 us; 4000 x 14336 45 us; rows that start anywhere 65536
+// x 1001 46.2 us, 8192 x 4001 36.6 us; matrices that lie differently 8192 x 4096 49.3 us;
+// 8192 x 20000 285 us (a barrier of two CTAs a row).  The arithmetic goes two columns an
+// instruction (pairs.cuh).
 #pragma once
 
 #include "layer_norm.cuh"
@@ -52,6 +52,12 @@ struct RowStats {
 template <int MODE, int SHAPE>
 constexpr int fwd_warps = MODE == kAny && SHAPE != kTall ? 12 : 16;
 
+// CTAs an SM is to hold at least (0: what the compiler makes of it).  One element at a
+// time takes 208 registers otherwise: 65536 x 1001 bf16, rows 1002 apart, 84.9 us against
+// 105.9.
+template <int SPAN, int OWN, int MODE, int SHAPE>
+constexpr int fwd_ctas = SHAPE == kLanes && SPAN == 32 && OWN <= 32 && MODE == kAny ? 3 : 0;
+
 // Bytes of a warp's part of a row in the ring.
 template <typename T, int SPAN, int NV, int E, int MODE>
 struct FwdStage {
@@ -63,12 +69,15 @@ struct FwdStage<T, SPAN, NV, 1, kAny> {
 };
 
 template <typename T, int SPAN, int NV, int E, int S, int MODE, bool SAVE, int SHAPE>
-__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warps<MODE, SHAPE>) norm_fwd_kernel(NormFwdParams p, int ctas) {
+__global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warps<MODE, SHAPE>,
+                                  fwd_ctas<SPAN, NV * E, MODE, SHAPE>)
+    norm_fwd_kernel(NormFwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Slot = UnitSlot<T, E, MODE, 32>;
   using Image = RowImage<T, SPAN, NV>;            // kAny
   constexpr bool kRest = sizeof(T) == 4, CL = Cols::kClustered, kMulti = Cols::kMulti;
   constexpr bool kEdges = norm_edges<SPAN, MODE>;
+  constexpr int kOwn = NV * E, G = E == 1 ? 2 : E, kGroups = kOwn / G;   // columns that are worked on together
   constexpr int kSpan = SPAN, kStage = FwdStage<T, SPAN, NV, E, MODE>::kBytes;
   static_assert(!SAVE || MODE == kAligned);
   using Ex = Exchange<kRest ? 3 : 2, SHAPE>;
@@ -105,9 +114,16 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warp
   wait_for_previous();
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch();
-  float w[NV * E], b[NV * E];
-  load_vector(cs, p.w, p.w_dtype, 1.f, w);
-  load_vector(cs, p.b, p.w_dtype, 0.f, b);
+  f32x2 w[kOwn / 2], b[kOwn / 2];
+  {
+    float v[kOwn];
+    load_vector(cs, p.w, p.w_dtype, 1.f, v);
+#pragma unroll
+    for (int k = 0; k < kOwn / 2; ++k) w[k] = pair(v[2 * k], v[2 * k + 1]);
+    load_vector(cs, p.b, p.w_dtype, 0.f, v);
+#pragma unroll
+    for (int k = 0; k < kOwn / 2; ++k) b[k] = pair(v[2 * k], v[2 * k + 1]);
+  }
   // columns of a warp of the row, as the exchange numbers them
   auto columns_of = [&](int warp) {
     if constexpr (!kMulti) return static_cast<float>(p.cols);
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warp
     fetch();
     const bool active = SPAN == 32 || row < p.rows;
     cp_async_wait<S - 1>();
-    float v[NV * E], part[NV];
+    f32x2 v[kOwn / 2], part[kGroups];
     float xe = 0.f;                         // this lane's element of the row's ends
     if constexpr (kEdges) {
       __syncwarp();                         // other lanes copied it
@@ -152,45 +168,58 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warp
       at = Image::place(from, lane, x);
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
+      float x[G];
       if constexpr (MODE == kAny) {
-        v[i] = Image::elem(at, i);
+        x[0] = Image::elem(at, 2 * i);
+        x[1] = Image::elem(at, 2 * i + 1);
       } else {
         Unit<T, E> u = Slot::finish(from + i * Slot::kBytes, lane);
         if (MODE == kPhase && !kEdges && !cs.whole(i)) u.keep(cs.lo - cs.col(i), cs.left(i));
-        u.get(v + E * i);
+        u.get(x);
       }
-      part[i] = tree_sum<E>(v + E * i);
+#pragma unroll
+      for (int k = 0; k < G / 2; ++k) v[G / 2 * i + k] = pair(x[2 * k], x[2 * k + 1]);
+      part[i] = tree_pairs<G / 2>(v + G / 2 * i);
     }
-    if constexpr (kEdges) part[0] += xe;
-    const float sum = span_sum<kSpan>(tree_sum_any<NV>(part));
+    const float sum = span_sum<kSpan>(pair_sum(tree_pairs<kGroups>(part)) + xe);
     const float m = divide(sum, n_w, inv_w);
-    float p2[NV], p1[NV];
+    const f32x2 minus_m = pair(-m);
+    f32x2 squares[2] = {pair(0.f), pair(0.f)}, p1[kGroups];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[E];
+    for (int i = 0; i < kGroups; ++i) {
+      f32x2 e[G / 2];
 #pragma unroll
-      for (int j = 0; j < E; ++j) e[j] = v[E * i + j] - m;
-      if (MODE == kPhase && !kEdges && !cs.whole(i)) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = cs.has(i, j) ? e[j] : 0.f;
+      for (int k = 0; k < G / 2; ++k) {
+        e[k] = add2(v[G / 2 * i + k], minus_m);
+        if constexpr (MODE == kAny) {
+          e[k] = keep_pair(e[k], cs.whole(2 * i), cs.whole(2 * i + 1));
+        } else if (MODE == kPhase && !kEdges) {
+          if (!cs.whole(i)) e[k] = keep_pair(e[k], cs.has(i, 2 * k), cs.has(i, 2 * k + 1));
+        }
       }
-      p2[i] = 0.f;
+      if constexpr (G == 2) {
+        squares[i & 1] = fma2(*e, *e, squares[i & 1]);
+        if constexpr (kRest) p1[i] = *e;
+      } else {
+        f32x2 q = mul2(e[0], e[0]);
 #pragma unroll
-      for (int j = 0; j < E; ++j) p2[i] = fmaf(e[j], e[j], p2[i]);
-      if constexpr (kRest) p1[i] = tree_sum<E>(e);
-      if ((MODE != kPhase || kEdges) && !cs.whole(i)) {
-        p2[i] = 0.f;
-        if constexpr (kRest) p1[i] = 0.f;
+        for (int k = 1; k < G / 2; ++k) q = fma2(e[k], e[k], q);
+        if constexpr (kRest) p1[i] = tree_pairs<G / 2>(e);
+        if ((MODE == kAligned || kEdges) && !cs.whole(i)) {
+          q = pair(0.f);
+          if constexpr (kRest) p1[i] = pair(0.f);
+        }
+        squares[i & 1] = add2(squares[i & 1], q);
       }
     }
+    float sq = pair_sum(add2(squares[0], squares[1])), rest = 0.f;
+    if constexpr (kRest) rest = pair_sum(tree_pairs<kGroups>(p1));
     if constexpr (kEdges) {
       const float e = edge.on ? xe - m : 0.f;
-      p2[0] = fmaf(e, e, p2[0]);
-      if constexpr (kRest) p1[0] += e;
+      sq = fmaf(e, e, sq);
+      if constexpr (kRest) rest += e;
     }
-    float sq = tree_sum_any<NV>(p2), rest = 0.f;
-    if constexpr (kRest) rest = tree_sum_any<NV>(p1);
     RowStats st;
     if constexpr (!kMulti) {
       sq = span_sum<kSpan>(sq);
@@ -254,15 +283,17 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : 32 * fwd_warp
       if (p.rstd) p.rstd[row] = st.rstd;
     }
     void* y = static_cast<char*>(p.Y) + row * p.ldy * (p.y_dtype == METIS_BF16 ? 2 : 4);
+    const f32x2 minus_m0 = pair(-st.m0), rr = pair(st.rstd), off = pair(st.off);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float o[E];
+    for (int i = 0; i < kGroups; ++i) {
+      float o[G];
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int k = E * i + j;
-        o[j] = fmaf(fmaf(v[k] - st.m0, st.rstd, st.off), w[k], b[k]);
+      for (int k = 0; k < G / 2; ++k) {
+        const int j = G / 2 * i + k;
+        unpair(fma2(fma2(add2(v[j], minus_m0), rr, off), w[j], b[j]), o[2 * k], o[2 * k + 1]);
       }
-      store_row_unit_any(cs, y, p.y_dtype, o, i, active);
+      store_row_unit_any(cs, y, p.y_dtype, o, G / E * i, active);
+      if constexpr (E == 1) store_row_unit_any(cs, y, p.y_dtype, o + 1, 2 * i + 1, active);
     }
     if constexpr (kEdges) {
       if (edge.on) store_any(y, p.y_dtype, edge.col, fmaf(fmaf(xe - st.m0, st.rstd, st.off), we, be));

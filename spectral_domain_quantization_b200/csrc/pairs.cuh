@@ -39,5 +39,21 @@ MDEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+// v's halves, or 0
+MDEV f32x2 keep_pair(f32x2 v, bool first, bool second) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pair(first ? lo : 0.f, second ? hi : 0.f);
+}
+// Sum of N pairs in a balanced tree: a value passes through about log2 N additions,
+// so an outlier does not cost the values after it their bits.
+template <int N>
+MDEV f32x2 tree_pairs(const f32x2* v) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    return add2(tree_pairs<N / 2>(v), tree_pairs<N - N / 2>(v + N / 2));
+  }
+}
 
 }  // namespace metis
