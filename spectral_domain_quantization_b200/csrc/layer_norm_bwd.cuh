@@ -10,7 +10,7 @@
 //
 // Measured, bf16 unless said: 16384 x 4096 77.3 us, 5.2 TB/s (a copy does 6.55), float32
 // 126 us (6.4 TB/s), from 8 bits with a float32 gradient 98.8 us (6.1 TB/s); 8192 x 4096
-// from 8 bits 42.8 us; 65536 x 1024 72.2 us; 4000 x 14336 89 us; rows that start anywhere
+// from 8 bits 42.8 us; 65536 x 1024 71.8 us; 4000 x 14336 91 us; rows that start anywhere
 // 65536 x 1001 86.9 us, 8192 x 4001 58.7 us; matrices that lie differently 8192 x 4096
 // 66.3 us.  The arithmetic goes two columns an instruction (pairs.cuh); what is left
 // short of the copy's rate waits for rows with 12 to 16 warps an SM, since the sums of
@@ -96,11 +96,19 @@ struct BwdStage<Act8Tag, TG, SPAN, NV, 1, kAny> {
 constexpr int kBwdWarps = 8;       // of a CTA
 constexpr int kTallWarps = 16;
 
-// (Aligned bf16 rows of a CTA are held to 128 registers, four CTAs of 4096 columns an
-// SM: 4096 x 8192 takes 47.4 us so against 62.5 with 148 registers.)
+// CTAs of 8 warps an SM is to hold at least (0: what the compiler makes of it), so 128
+// registers a thread: four CTAs of 4096 columns an SM instead of three, 4096 x 8192 bf16
+// 47.4 us against 62.5; in clusters 4000 x 14336 bf16 91.2 against 129.5,
+// float32 125.5 against 155.7.  (Float32 rows
+// of one CTA have no use for it: 16384 x 2048 73.0 against 70.5.)
+template <typename TX, int E, int MODE, int SHAPE>
+constexpr int bwd_ctas = MODE == kAligned && !std::is_same_v<TX, Act8Tag> && (SHAPE == kCluster || (SHAPE == kCta && E == 8))
+                             ? 2
+                             : 0;
+
 template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, int SHAPE>
 __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256),
-                                  SHAPE == kCta && MODE == kAligned && E == 8 && !std::is_same_v<TX, Act8Tag> ? 2 : 0)
+                                  bwd_ctas<TX, E, MODE, SHAPE>)
     norm_bwd_kernel(NormBwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
@@ -506,7 +514,7 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
   // A cluster's CTAs of more than 5 warps leave an SM room for one, and half its
   // threads idle: from there one CTA of 16 warps has the row, where the arithmetic is
   // what bounds it.  4000 rows from 8 bits: 14336 columns 94.5 us against 123.7 in a
-  // cluster, 10240 columns 82.6 against 77.1; bf16 14335 columns 113 against 157, 8449
+  // cluster, 10240 columns 82.6 against 77.1; bf16 14335 columns 111 against 157, 8449
   // columns 92.3 against 90.2.  (bf16 that lies aligned: 94.6 against 89.1 with 14336.)
   if constexpr (E == 8 && (MODE == kPhase || std::is_same_v<TX, Act8Tag>)) {
     if (cols > 10 * kWarpCols && cols <= kTallWarps * kWarpCols)
