@@ -326,7 +326,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         x.centered(p.saved.fmt, minus, d);
       }
     };
-    float s1 = 0.f, s2 = 0.f;               // sums of g xh and of g
+    // sums of g xh and of g rstd.  rstd goes to dy, not to x - mean: a column that is
+    // not the row's has x = 0 and dy = 0, and dy (0 - mean) is 0 for any mean, where
+    // (0 - mean) rstd may be past float32 and 0 times it NaN
+    float s1 = 0.f, s2 = 0.f;
     float xe = 0.f, ge = 0.f;               // this lane's element of the row's ends: x - mean, and dy
     if constexpr (kEdges) {
       __syncwarp();                         // other lanes copied it
@@ -344,10 +347,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         GS::clear(from + edge.last_unit * Stage::kOne, lane);
         XS::clear(from + edge.last_unit * Stage::kOne + GS::kBytes, lane);
       }
-      const float xh = xe * rstd, gk = ge * we;
-      s1 = gk * xh;
-      s2 = gk;
-      awe = fmaf(ge, xh, awe);
+      const float r = ge * rstd, gr = r * we;
+      s1 = gr * xe;
+      s2 = gr;
+      awe = fmaf(r, xe, awe);
       abe += ge;
     }
     f32x2 t1 = pair(s1, 0.f), t2 = pair(s2, 0.f);
@@ -361,10 +364,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
 #pragma unroll
       for (int j = 0; j < G / 2; ++j) {
         const int k = G / 2 * i + j;
-        const f32x2 xh = mul2(d[j], rr), gk = mul2(dy[j], wu[j]);
-        t1 = fma2(gk, xh, t1);
-        t2 = add2(t2, gk);
-        aw[k] = fma2(dy[j], xh, aw[k]);
+        const f32x2 r = mul2(dy[j], rr), gr = mul2(r, wu[j]);
+        t1 = fma2(gr, d[j], t1);
+        t2 = add2(t2, gr);
+        aw[k] = fma2(r, d[j], aw[k]);
         ab[k] = add2(ab[k], dy[j]);
       }
     }
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         }
       }
       // dx = rstd g + (x - mean) kd + k0
-      const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -rstd * (c2 * p.inv_n);
+      const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -(c2 * p.inv_n);
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
       const f32x2 kd2 = pair(kd), k02 = pair(k0);
 #pragma unroll
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         g_group(i, dy);
 #pragma unroll
         for (int j = 0; j < G / 2; ++j)
-          unpair(fma2(mul2(dy[j], wu[j]), rr, fma2(d[j], kd2, k02)), o[2 * j], o[2 * j + 1]);
+          unpair(fma2(mul2(dy[j], rr), wu[j], fma2(d[j], kd2, k02)), o[2 * j], o[2 * j + 1]);
         store_row_unit_any(cs, out, p.dx_dtype, o, G / E * i, active);
         if constexpr (E == 1) store_row_unit_any(cs, out, p.dx_dtype, o + 1, 2 * i + 1, active);
       }
