@@ -143,6 +143,11 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // so a CTA of the SM, 8192 x 4095 bf16 99 us against 74; rows of 40 columns a thread
   // have no register left for it either)
   constexpr bool kInside = MODE == kPhase && !(E == 8 && (SHAPE == kCta || NV > 4));
+  // (kDerived: the loop sets both.  Clusters held to 128 registers spill otherwise, 4000
+  // x 14336 float32 118.6 us against 124.9, and from 8 bits with a float32 gradient take
+  // 193 registers, 147.8 against 153.9; 8-bit rows of lanes 100000 x 512 60.2 against
+  // 63.0.  With the rows of a CTA it takes longer: 16384 x 4096 bf16 81.7 against 76.4.)
+  constexpr bool kDerived = CL || (!kDense && !kMulti);
   int64_t fetch_row = cs.row;
   uint32_t into = ring0;
   auto fetch = [&] {
@@ -181,8 +186,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
       }
     }
     cp_async_commit();
-    fetch_row += cs.step;
-    into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
+    if constexpr (!kDerived) {
+      fetch_row += cs.step;
+      into = into + kStage == ring0 + S * kStage ? ring0 : into + kStage;
+    }
   };
   float next_mean = 0.f, next_rstd = 0.f;
   // kAny: lane t has the scale code of the t-th 8-bit block of its row's lanes
@@ -246,6 +253,11 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // all of the warp
   for (int64_t row = cs.row; SPAN == 32 ? row < p.rows : row - (lane / SPAN) < p.rows; row += cs.step) {
     if constexpr (MODE == kAny) __syncwarp();      // every lane has read the stage that is copied to
+    if constexpr (kDerived) {
+      static_assert(S == 2);
+      fetch_row = row + cs.step;
+      into = 2 * ring0 + kStage - from;
+    }
     fetch();
     const bool active = SPAN == 32 || row < p.rows;
     const float mean = next_mean, rstd = next_rstd;
@@ -418,7 +430,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         if (edge.on) store_any(out, p.dx_dtype, edge.col, fmaf(ge * we, rstd, fmaf(xe, kd, k0)));
       }
     }
-    from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
+    if constexpr (kDerived)
+      from = into;
+    else
+      from = from + kStage == ring0 + S * kStage ? ring0 : from + kStage;
   }
   cp_async_wait<0>();
   launch_next();   // the kernel that adds the partial sums waits for this one's end
