@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_rows_kernel(NormBwdParams 
       s1 = fmaf(g, (wide_x(p, row, c) - mean) * rstd, s1);
       s2 += g;
     }
-    const float kd = -rstd * rstd * (cta_sum(s1, buf) * p.inv_n), k0 = -rstd * (cta_sum(s2, buf) * p.inv_n);
+    const float kd = -rstd * (rstd * (cta_sum(s1, buf) * p.inv_n)), k0 = -rstd * (cta_sum(s2, buf) * p.inv_n);
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
       const float g = load_any(p.dY, p.g_dtype, row * p.ldg + c) * (p.w ? load_any(p.w, p.w_dtype, c) : 1.f);
       store_any(p.dX, p.dx_dtype, row * p.ldd + c, fmaf(g, rstd, fmaf(wide_x(p, row, c) - mean, kd, k0)));

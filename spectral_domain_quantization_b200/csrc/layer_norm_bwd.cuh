@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
         }
       }
       // dx = rstd g + (x - mean) kd + k0
-      const float kd = -rstd * rstd * (c1 * p.inv_n), k0 = -(c2 * p.inv_n);
+      const float kd = -rstd * (rstd * (c1 * p.inv_n)), k0 = -(c2 * p.inv_n);
       void* out = static_cast<char*>(p.dX) + row * p.ldd * (p.dx_dtype == METIS_BF16 ? 2 : 4);
       const f32x2 kd2 = pair(kd), k02 = pair(k0);
 #pragma unroll
