@@ -529,13 +529,19 @@ int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cuda
     if (cols <= 1280) return norm_bwd_go<TX, TG, 32, 40 / E, E, MODE, kLanes>(p, parts, occ, num_sms, s);
   }
   if (cols <= kBwdWarps * kWarpCols) return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCta>(p, parts, occ, num_sms, s);
-  // A cluster's CTAs of more than 5 warps leave an SM room for one, and half its
-  // threads idle: from there one CTA of 16 warps has the row, where the arithmetic is
-  // what bounds it.  4000 rows from 8 bits: 14336 columns 94.5 us against 123.7 in a
-  // cluster, 10240 columns 82.6 against 77.1; bf16 14335 columns 111 against 157, 8449
-  // columns 92.3 against 90.2.  (bf16 that lies aligned: 94.6 against 89.1 with 14336.)
-  if constexpr (E == 8 && (MODE == kPhase || std::is_same_v<TX, Act8Tag>)) {
-    if (cols > 10 * kWarpCols && cols <= kTallWarps * kWarpCols)
+  // One CTA of up to 16 warps in place of a cluster of two, for long rows (4000 of them
+  // unless said; one CTA against a cluster, us).  Shifted bf16 rows: from 10 warps on,
+  // since shorter ones gain little and lose where the rows are few (8449 columns 83.2 and
+  // 86.5, 9001 85.6 and 88.2, 333 rows of 9001 25.0 and 22.7; 10239 88.1 and 93.5, 12279
+  // 102.1 and 102.0, 14335 108.0 and 153.8).  From 8 bits: where a cluster's CTAs have more
+  // than 6 warps, so that an SM holds one of them (bf16 gradient: 9000 columns 78.9 and
+  // 74.8, 10240 76.6 and 76.0, 12288 86.7 and 80.2, 12320 86.8 and 118.7, 14336 88.4 and
+  // 120.4; float32 gradient: 9000 98.2 and 88.5, 12288 105 and 95.0, 14336 109 and 148).
+  // Dense rows that lie aligned have clusters of two CTAs to an SM (bwd_ctas); the stages
+  // of the other shifted rows and the weights do not fit an SM's shared memory.
+  constexpr bool kKept = std::is_same_v<TX, Act8Tag>;
+  if constexpr ((kKept && E != 1) || (E == 8 && MODE == kPhase)) {
+    if (cols > (kKept ? 12 : 10) * kWarpCols && cols <= kTallWarps * kWarpCols)
       return norm_bwd_go<TX, TG, 32, NV, E, MODE, kTall>(p, parts, occ, num_sms, s);
   }
   return norm_bwd_go<TX, TG, 32, NV, E, MODE, kCluster>(p, parts, occ, num_sms, s);

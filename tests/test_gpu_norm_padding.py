@@ -39,3 +39,22 @@ def test_large_constant_row(cols, kind, gdtype, lie):
     got = api.layer_norm_bwd(dY, X if not a8 else r.saved, r.mean, r.rstd, w)
     assert all(torch.isfinite(t).all() for t in got)
     check_bwd(got, dY, x64, r.mean, r.rstd, w)
+
+
+@pytest.mark.parametrize("cols", [8200, 8449, 9001, 10239, 12281, 12288, 12320, 13000, 14335, 14336, 16377, 16384])
+@pytest.mark.parametrize("kind,gdtype", [("bf16", "bf16"), ("mxint8", "bf16"), ("mxint8", "f32"), ("mxfp8", "f32")])
+def test_long_rows(cols, kind, gdtype):
+    # rows of one CTA and of a cluster, fewer of them than an SM holds and more
+    for rows in (1, 5, 400):
+        x, dy, w, _ = data(rows, cols, seed=62)
+        a8 = kind.startswith("mx")
+        X, dY, w = mat(x, "bf16" if a8 else kind), mat(dy, gdtype), w.cuda()
+        r = api.layer_norm_fwd(X, w, save=kind if a8 else None)
+        given = r.saved if a8 else X
+        x64 = np64(X if not a8 else api.restore_act8(r.saved, torch.float32))
+        got = api.layer_norm_bwd(dY, given, r.mean, r.rstd, w)
+        check_bwd(got, dY, x64, r.mean, r.rstd, w)
+        # over dY, and one output alone: the same values
+        over = dY.clone()
+        part = api.layer_norm_bwd(over, given, r.mean, r.rstd, w, want_db=False, out=over)
+        assert torch.equal(over, got[0]) and torch.equal(part[1], got[1]) and part[2] is None
