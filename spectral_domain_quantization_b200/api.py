@@ -9,6 +9,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 
 import torch
 
@@ -171,10 +172,11 @@ def _dtype_code(t):
     raise TypeError("only bfloat16 and float32 inputs are supported")
 
 
-class _Workspace:
-    """Grow-only workspace per device and stream (allocated by torch, the
+class _Workspace(threading.local):
+    """Grow-only workspace per thread, device and stream (allocated by torch, the
     caller side), so that calls enqueued on different streams never share
-    scratch memory.  A call that is captured into a graph gets memory of its
+    scratch memory, nor do two threads' calls on one stream, whose kernels may
+    be enqueued in turn (ctypes releases the interpreter during a call).  A call that is captured into a graph gets memory of its
     own, from the graph's pool: graphs captured on one stream may be replayed
     at the same time, and live longer than a buffer that grows."""
 
@@ -205,8 +207,8 @@ _ws = _Workspace()
 
 def _call_with_workspace(fn, args_before_ws, args_after_ws, device, what, workspace=None):
     """Provide a workspace (the caller's uint8 tensor when given, else the
-    shared per-stream one, grown to the size the call asks for), then run the
-    call."""
+    thread's own for the stream, grown to the size the call asks for), then run
+    the call."""
     if workspace is None:
         ws = _ws.held(device)
         if ws is not None:
