@@ -242,10 +242,34 @@ def _fp4_bytes(fmt, outer, inner):
     return L.metis_fp4_codes_bytes(outer, inner), L.metis_fp4_scales_bytes(fmt, outer, inner)
 
 
+class _Ones(threading.local):
+    """Floats on the device that hold 1, each handed out once: the tensor scales of
+    MXFP4 results, which no kernel writes.  Filled many at a time on the stream they
+    are for, so that a result costs no launch of its own."""
+
+    def __init__(self):
+        self.ready = {}          # by device and stream: a tensor of ones, and how many are taken
+
+    def take(self, device):
+        """A tensor and the index of the 1 in it."""
+        if torch.cuda.is_current_stream_capturing():
+            return torch.ones(1, dtype=torch.float32, device=device), 0      # the graph's, as the codes are
+        key = (device.index, _stream_of(device.index))
+        have = self.ready.get(key)
+        if have is None or have[1] == have[0].numel():
+            have = self.ready[key] = [torch.ones(256, dtype=torch.float32, device=device), 0]
+        have[1] += 1
+        return have[0], have[1] - 1
+
+
+_ones = _Ones()
+
+
 class QTensor:
     """An FP4 matrix (outer x inner, blocks along inner) held in torch buffers:
     codes, scales and tensor_scale (1 for MXFP4), and scales_linear and inner_sum
-    or None."""
+    or None.  Those that a quantizer's call allocates are parts of one storage:
+    each keeps all of it alive, and is to be cloned before it is saved alone."""
 
     def __init__(self, fmt, outer, inner, device="cuda", linear=False, inner_sum=False, written=False):
         # written: for a call that writes all of it now.  codes, scales and
@@ -260,6 +284,8 @@ class QTensor:
             self._parts = (nc, at, ns, end)
             self._buf = torch.empty(end + 4, dtype=torch.uint8, device=device)
             self.device = self._buf.device
+            if self.fmt == MXFP4:
+                self._one = _ones.take(self.device)
         else:
             self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
             self.scales = torch.empty(ns, dtype=torch.uint8, device=device)
@@ -280,7 +306,8 @@ class QTensor:
             elif self.fmt == NVFP4:
                 self.tensor_scale = self._buf[end:].view(torch.float32)
             else:
-                self.tensor_scale = torch.ones(1, dtype=torch.float32, device=self.device)
+                ones, k = self._one
+                self.tensor_scale = ones[k:k + 1]
             return self.__dict__[name]
         raise AttributeError(name)
 
