@@ -463,8 +463,9 @@ METIS_API metis_status metis_act8_save(const void* X, int32_t dtype, int64_t row
 /*
  * metis_act8_restore -- the matrix that `in` holds, as METIS_BF16 or METIS_F32
  * (Y: rows x cols, leading dimension ld).  float32 holds every value exactly;
- * bf16 does too, down to its subnormals (METIS_MXFP8 blocks under 2^-124 may
- * round).  Errors as for metis_act8_save.
+ * bf16 does too, but for METIS_MXFP8 blocks whose maximum is under 2^-116: their
+ * smallest steps are under bf16's (2^-133) and round.  Errors as for
+ * metis_act8_save.
  */
 METIS_API metis_status metis_act8_restore(const metis_act8_tensor* in, void* Y, int32_t dtype, int64_t ld,
                                 void* stream);
