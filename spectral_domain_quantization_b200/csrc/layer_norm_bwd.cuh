@@ -97,18 +97,22 @@ constexpr int kBwdWarps = 8;       // of a CTA
 constexpr int kTallWarps = 16;
 
 // CTAs of 8 warps an SM is to hold at least (0: what the compiler makes of it), so 128
-// registers a thread: four CTAs of 4096 columns an SM instead of three, 4096 x 8192 bf16
-// 47.4 us against 62.5; in clusters 4000 x 14336 bf16 91.2 against 129.5,
-// float32 125.5 against 155.7.  (Float32 rows
-// of one CTA have no use for it: 16384 x 2048 73.0 against 70.5.)
-template <typename TX, int E, int MODE, int SHAPE>
-constexpr int bwd_ctas = MODE == kAligned && !std::is_same_v<TX, Act8Tag> && (SHAPE == kCluster || (SHAPE == kCta && E == 8))
+// registers a thread, in dense rows that lie aligned.  With and without, us: rows of one
+// CTA in bf16 4096 x 8192 47.4 and 64.2, 16384 x 4096 76.3 and 83.1; clusters 4000 x 14336
+// bf16 89.6 and 131.8, from float32 with a bf16 gradient 96.8 and 136.0, the other way
+// round 107.9 and 144.3.  Not where both are float32: the shared memory of the stages is
+// what an SM runs out of (clusters 4000 x 14336 119.1 and 115.9, 4000 x 9000 101.4 and
+// 97.5), nor in rows of one CTA with a float32 matrix (16384 x 2048 70.9 and 70.8).
+template <typename TX, typename TG, int E, int MODE, int SHAPE>
+constexpr int bwd_ctas = MODE == kAligned && !std::is_same_v<TX, Act8Tag> &&
+                                 ((SHAPE == kCluster && !(std::is_same_v<TX, float> && std::is_same_v<TG, float>)) ||
+                                  (SHAPE == kCta && E == 8))
                              ? 2
                              : 0;
 
 template <typename TX, typename TG, int SPAN, int NV, int E, int S, int MODE, int SHAPE>
 __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTall ? 512 : 256),
-                                  bwd_ctas<TX, E, MODE, SHAPE>)
+                                  bwd_ctas<TX, TG, E, MODE, SHAPE>)
     norm_bwd_kernel(NormBwdParams p, int ctas) {
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   using Stage = BwdStage<TX, TG, SPAN, NV, E, MODE>;
@@ -143,10 +147,10 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // so a CTA of the SM, 8192 x 4095 bf16 99 us against 74; rows of 40 columns a thread
   // have no register left for it either)
   constexpr bool kInside = MODE == kPhase && !(E == 8 && (SHAPE == kCta || NV > 4));
-  // (kDerived: the loop sets both.  Clusters held to 128 registers spill otherwise, 4000
-  // x 14336 float32 118.6 us against 124.9, and from 8 bits with a float32 gradient take
-  // 193 registers, 147.8 against 153.9; 8-bit rows of lanes 100000 x 512 60.2 against
-  // 63.0.  With the rows of a CTA it takes longer: 16384 x 4096 bf16 81.7 against 76.4.)
+  // (kDerived: the loop sets both, for want of registers.  Clusters so and with both
+  // carried, us: 4000 x 14336 float32 115.9 and 160.8, bf16 89.8 and 91.5, 4000 x 9000 from
+  // 8 bits with a float32 gradient 88.7 and 144.9; 8-bit rows of lanes 100000 x 512 60.2
+  // and 63.0.  Rows of a CTA take longer so: 16384 x 4096 bf16 81.7 and 76.4.)
   constexpr bool kDerived = CL || (!kDense && !kMulti);
   int64_t fetch_row = cs.row;
   uint32_t into = ring0;
