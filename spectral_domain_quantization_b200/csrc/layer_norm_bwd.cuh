@@ -143,10 +143,6 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
   // row `fetch_row` into the stage at `into`; what a row needs besides, its mean
   // and rstd and the scale codes of its 8-bit blocks, goes into registers one row
   // ahead
-  // (a second copy of the loads costs kCta's 16-byte units 40 registers a thread and
-  // so a CTA of the SM, 8192 x 4095 bf16 99 us against 74; rows of 40 columns a thread
-  // have no register left for it either)
-  constexpr bool kInside = MODE == kPhase && !(E == 8 && (SHAPE == kCta || NV > 4));
   // (kDerived: the loop sets both, for want of registers.  Clusters so and with both
   // carried, us: 4000 x 14336 float32 115.9 and 160.8, bf16 89.8 and 91.5, 4000 x 9000 from
   // 8 bits with a float32 gradient 88.7 and 144.9; 8-bit rows of lanes 100000 x 512 60.2
@@ -158,7 +154,7 @@ __global__ void __launch_bounds__(SHAPE == kLanes ? kLaneThreads : (SHAPE == kTa
     const bool on = fetch_row < p.rows;
     if (SPAN < 32 || on) {
       const TG* g = dY + fetch_row * p.ldg;
-      const bool inside = kInside && on && row_inside(g, p.cols, gspan) &&
+      const bool inside = MODE == kPhase && on && row_inside(g, p.cols, gspan) &&
                           (!kDense || row_inside(X + fetch_row * p.ldx, p.cols, xspan));
       if constexpr (MODE == kAny) {
         const int n = on ? cs.left(0) + cs.t : 0, c = cs.col(0) - cs.t;
