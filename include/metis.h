@@ -499,12 +499,17 @@ METIS_API metis_status metis_act8_quantize_fp4(const metis_act8_tensor* in, int3
  *           not overlap it otherwise.
  *   mean, rstd  device, rows floats each, or NULL.
  *   saved   optional (NULL: none): X in 8 bits (metis_act8_tensor, rows x cols),
- *           the bytes metis_act8_save writes, from the same pass over X.
+ *           the bytes metis_act8_save writes.  From the same pass over X where
+ *           the rows of X and Y begin on 16-byte boundaries and cols is a
+ *           multiple of 8 and at most 32768; metis_act8_save's kernel reads X
+ *           once more otherwise.
  * X, Y and ld need no more alignment than their elements; rows may be 0.
  * Statistics are float32 sums, in a fixed order that depends on the sizes, types,
  * alignments and the device alone; neither the variance nor the mean of a row far
  * from zero is a difference of large sums.
- * A row with an infinity or a NaN gives NaN in that row alone.  No workspace.
+ * A row with an infinity or a NaN gives NaN in that row alone.  So does a row whose
+ * values' sum is past float32's range; one whose squared deviations' sum is (a
+ * deviation of 1.9e19 is enough) has rstd = 0 and Y = bias.  No workspace.
  * Errors: METIS_ERR_NULL, METIS_ERR_ARG (dtypes, eps, fmt), METIS_ERR_SHAPE,
  * METIS_ERR_ALIGN, METIS_ERR_UNSUPPORTED, METIS_ERR_CUDA.
  */

@@ -838,9 +838,11 @@ def layer_norm_fwd(X, weight=None, bias=None, eps=1e-5, out_dtype=None, save=Non
 
     X: 2-D bf16/f32 CUDA tensor, any row stride; weight, bias: vectors (bf16 or
     f32) or None.  out_dtype: dtype of Y (X's).  save: "mxint8" or "mxfp8" also
-    keeps X in 8 bits, from the same pass; pass the result's ``saved`` to
-    layer_norm_bwd in place of X.  stats=False: Y alone (inference).  out: Y's
-    tensor (X itself is allowed if it has Y's dtype)."""
+    keeps X in 8 bits; pass the result's ``saved`` to layer_norm_bwd in place of
+    X.  (One pass over X where the rows of X and Y begin on 16-byte boundaries
+    and are a multiple of 8 columns, at most 32768; save_act8's kernel first
+    otherwise.)  stats=False: Y alone (inference).  out: Y's tensor (X itself is
+    allowed if it has Y's dtype, no other overlap)."""
     ldx = _matrix(X, "X")
     dev = X.device
     rows, cols = X.shape
@@ -877,7 +879,8 @@ def layer_norm_bwd(dY, X, mean, rstd, weight=None, out_dtype=None, want_dx=True,
 
     X: the forward's input, or the Act8 it kept; mean, rstd: the forward's.
     out_dtype: dtype of dX (dY's); dweight and dbias are float32.  An output
-    that is not wanted is None."""
+    that is not wanted is None.  out: dX's tensor (dY itself is allowed if it has
+    dX's dtype, no other overlap with an input)."""
     ldg = _matrix(dY, "dY")
     dev = dY.device
     rows, cols = dY.shape

@@ -1,14 +1,15 @@
 // What the layer norm's forward and backward kernels share: how rows are spread
 // over threads, and the sums over a row.
 //
-// A row is held in registers: by SPAN lanes of a warp (up to 1024 columns), by the
-// W warps of a CTA, 1024 columns each, or by a cluster of CTAs that take a slice of
-// the columns each (sums meet in distributed shared memory).  Each thread has NV
-// units of E consecutive columns (rows.cuh), the same columns in every row: 32
-// columns a thread, so what a row costs besides its elements (reductions, roots,
-// addresses) is spread over many.  E is 8 where every matrix is bf16 (16-byte words)
-// and 4 where one is float32, so that a warp's words are contiguous.  The rows to
-// come wait in a ring in shared memory, each warp's part in a ring of its own.
+// A row is held in registers: by SPAN lanes of a warp (up to 1024 columns; 1536
+// forward, and 1280 backward in units of 8), by the W warps of a CTA, 1024 columns
+// each, or by a cluster of CTAs that take a slice of the columns each (sums meet in
+// distributed shared memory).  Each thread has NV units of E consecutive columns
+// (rows.cuh), the same columns in every row: 32 columns a thread, so what a row costs
+// besides its elements (reductions, roots, addresses) is spread over many.  E is 8
+// where every matrix is bf16 (16-byte words) and 4 where one is float32, so that a
+// warp's words are contiguous.  The rows to come wait in a ring in shared memory, each
+// warp's part in a ring of its own.
 #pragma once
 
 #include <atomic>

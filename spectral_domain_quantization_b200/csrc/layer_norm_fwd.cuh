@@ -1,5 +1,7 @@
 // Layer norm, forward: y = (x - mean) rstd w + b over the columns of each row,
-// optionally keeping x in 8 bits from the same pass.
+// optionally keeping x in 8 bits from the same pass (rows that lie aligned; others
+// are copied by act8_save_kernel first: 16384 x 1027 bf16 39.1 us with the copy, of
+// which the norm takes 20.4, 8192 x 4001 68.0 and 36.6).
 //
 // Bound by HBM: every element is read once and written once (and once more as
 // 1 + 1/32 bytes with the 8-bit copy).  A warp sums its part of the row, then the

@@ -26,3 +26,26 @@ def test_zero_row_and_smallest_eps(cols, dtype):
     got = api.layer_norm_bwd(dY, X, r.mean, r.rstd, w)
     assert torch.isfinite(got[0]).all()
     check_bwd(got, dY, np64(X), r.mean, r.rstd, w)
+
+
+@pytest.mark.parametrize("cols", [40, 1000, 1001, 4096, 9001, 14336, 33000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sums_past_float32(cols, dtype):
+    # what the header says of such rows, and nothing of it in the others
+    x, dy, w, b = data(8, cols, seed=71)
+    X, dY, w, b = mat(x, dtype), mat(dy, dtype), w.cuda(), b.cuda()
+    rest = torch.tensor([0, 1, 3, 5, 7], device="cuda")
+    clean = api.layer_norm_fwd(X, w, b)
+    dclean = api.layer_norm_bwd(dY, X, clean.mean, clean.rstd, w)
+    X[2] *= 1e25                          # squared deviations
+    X[4] = 3e38                           # the sum of the values
+    X[6] = -1e35
+    X[6, ::2] = 1e35                      # squares again, of a row whose sum stays
+    r = api.layer_norm_fwd(X, w, b)
+    assert torch.equal(r.Y[rest], clean.Y[rest]) and torch.equal(r.rstd[rest], clean.rstd[rest])
+    assert torch.isnan(r.Y[4]).all() and not torch.isfinite(r.mean[4])
+    for k in (2, 6):
+        assert float(r.rstd[k]) == 0 and torch.equal(r.Y[k], b.to(r.Y.dtype))
+    dX = api.layer_norm_bwd(dY, X, r.mean, r.rstd, w)[0]
+    assert torch.equal(dX[rest], dclean[0][rest])
+    assert not dX[2].any() and not dX[6].any() and torch.isnan(dX[4]).all()
