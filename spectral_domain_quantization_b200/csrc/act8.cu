@@ -207,7 +207,9 @@ int occupancy(const void* kernel, size_t smem = 0) {
   return per_sm;
 }
 
-// no more CTAs than are resident at once: the loops are grid-strided
+// no more CTAs than are resident at once (the loops are grid-strided), and than the
+// maximum has slots.  Only the copy writes those, but the way back gains nothing from the
+// 160 more that would fit: 16384 x 14336 bf16 130.4 us with them against 127.5.
 int grid_for(int per_sm, int64_t ctas, int num_sms) {
   const int64_t most = imin64(static_cast<int64_t>(num_sms) * per_sm, METIS_ACT8_AMAX);
   return static_cast<int>(imax64(1, imin64(ctas, most)));
@@ -361,10 +363,11 @@ struct Tile {
 //    for 8 rows, by shuffle.  The codes of a column are put together in shared
 //    memory and leave as contiguous 64 (NVFP4) or 128 bytes a column.
 // 16384 x 14336: MXINT8 to NVFP4 115 us along the rows, 107 along the columns (3.3 and
-// 3.5 TB/s); MXFP8 to MXFP4 92 and 92 us (4.0 TB/s).  Bound by the arithmetic (an FP4
-// code of 4.5 bits out of 8.25 in leaves few bytes to hide it behind): 57 to 62 % of the
-// issue slots taken by 16 warps an SM; 24 warps take longer (136 us along the rows),
-// since less of the rows to come fits beside them.
+// 3.5 TB/s); MXFP8 to MXFP4 92 and 92 us (4.0 TB/s); 8192 x 4096 to NVFP4 21.0 and 20.1.
+// Neither HBM nor the issue slots are full (57 to 62 % of those, by 16 warps an SM): the
+// conversion, scaling, maximum and encoding of an element are scalar instructions that
+// depend on one another, and a warp has few of them in flight.  24 warps an SM take
+// longer, since 80 registers a thread spill (NVFP4 123 us along the rows, MXFP4 130).
 template <int FMT8, int FMT4, int AXIS>
 __global__ void __launch_bounds__(kThreads, 2) act8_quantize_kernel(Act8QuantParams p) {
   constexpr int kBlk = FMT4 == METIS_NVFP4 ? 16 : 32;

@@ -41,7 +41,7 @@ MDEV float wide_x(const NormBwdParams& p, int64_t row, int c) {
 }
 
 // Rows wider than a cluster holds.  dw and db: a thread a column, over the rows
-// y, y + gridDim.y, ...  (2000 x 40000 bf16: 727 us with the next kernel, 0.7 TB/s.)
+// y, y + gridDim.y, ...  (2000 x 40000 bf16: 729 us with the next kernel, 0.7 TB/s.)
 __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(NormBwdParams p) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= p.cols) return;

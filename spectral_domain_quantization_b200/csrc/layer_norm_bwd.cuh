@@ -8,13 +8,15 @@
 // sees, so dw and db are running sums in its registers; a CTA's rows end as one
 // row of partial sums, and a second kernel adds those in a fixed order.
 //
-// Measured, bf16 unless said: 16384 x 4096 77.3 us, 5.2 TB/s (a copy does 6.55), float32
-// 126 us (6.4 TB/s), from 8 bits with a float32 gradient 98.8 us (6.1 TB/s); 8192 x 4096
-// from 8 bits 42.8 us; 65536 x 1024 71.8 us; 4000 x 14336 91 us; rows that start anywhere
-// 65536 x 1001 86.9 us, 8192 x 4001 58.7 us; matrices that lie differently 8192 x 4096
-// 66.3 us.  The arithmetic goes two columns an instruction (pairs.cuh); what is left
-// short of the copy's rate waits for rows with 12 to 16 warps an SM, since the sums of
-// 32 columns a thread take 64 registers and the weights 32.
+// Measured, bf16 unless said: 16384 x 4096 76.4 us, 5.3 TB/s (a copy does 6.55), float32
+// 127 us (6.3 TB/s), from 8 bits with a float32 gradient 99.7 us (6.1 TB/s); 8192 x 4096
+// 46.0 us, from 8 bits 42.8 us; 65536 x 1024 72.4 us; 4000 x 14336 89.1 us, float32 115 us;
+// rows that start anywhere 65536 x 1001 86.3 us, 8192 x 4001 58.1 us, 16384 x 1027 34.3
+// us; matrices that lie differently 8192 x 4096 65.9 us.  The arithmetic goes two columns
+// an instruction (pairs.cuh); what is left short of the copy's rate waits for rows with
+// 12 to 16 warps an SM, since the sums of 32 columns a thread take 64 registers and the
+// weights 32 (kTall keeps the weights in shared memory; the other shapes were not tried
+// so).
 #pragma once
 
 #include "layer_norm.cuh"
@@ -489,8 +491,8 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
   using Cols = NormCols<SPAN, NV, E, MODE, SHAPE>;
   constexpr int kStage = BwdStage<TX, TG, SPAN, NV, E, MODE>::kBytes;
   constexpr int kGather = SHAPE == kLanes && Cols::kRows > 1 ? 32 * NV * E * 4 : 0;   // of a warp, when the ring is done
-  // two stages and the CTAs that then fit an SM: three stages take 78.6 us against
-  // 77.1 on 16384 x 4096 bf16, and 144 against 126 in float32
+  // two stages and the CTAs that then fit an SM: three stages take 77.2 us against
+  // 76.3 on 16384 x 4096 bf16, and 144 against 127 in float32
   constexpr int S = 2;
   // the weights, or the elements of an 8-bit row that lies anywhere
   constexpr int kStaged = SHAPE == kTall ? 4 * kWarpCols : (MODE == kAny && std::is_same_v<TX, Act8Tag> ? 128 * NV : 0);
@@ -515,7 +517,7 @@ int norm_bwd_go(const NormBwdParams& params, int parts, bool occupancy, int num_
 
 // E columns a unit, 32 a thread (16 where a row has 64 or fewer; 40 where that saves
 // the row's second warp and its sums still fit the registers: 16384 x 1280 bf16 takes
-// 30.1 us so against 40.9, 16384 x 1027 41.7 against 54.0).
+// 29.6 us so against 40.7, 16384 x 1027 34.3 against 50.3).
 template <typename TX, typename TG, int E, int MODE>
 int norm_bwd_cols(const NormBwdParams& p, int parts, bool occ, int num_sms, cudaStream_t s) {
   constexpr int NV = 32 / E, L = E == 8 ? 4 : 8;
